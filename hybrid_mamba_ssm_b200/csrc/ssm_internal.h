@@ -138,6 +138,111 @@ struct GatedNormArgs {
 };
 cudaError_t launch_gated_rmsnorm(const GatedNormArgs &a, cudaStream_t stream);
 
+// Per-channel selective scan (prefill, the forward pass of a training step)
+// and its gradient.  Activations are rows of `dim` (or ngroups * d_state)
+// values, one per token, `*_stride` elements apart.
+struct SelScanArgs {
+    int nseq, seqlen;             // seqlen = T when cu_seqlens is given
+    const int32_t *cu_seqlens;
+    int dim, d_state, ngroups;
+    int in_bf16, dt_bf16, y_bf16;
+    const void *x, *dt, *B, *C, *z;   // z nullptr: no gate
+    long x_stride, dt_stride, B_stride, C_stride, z_stride;
+    const float *A;               // [dim][d_state]
+    const float *D;               // [dim] or nullptr
+    DtParams dtp;
+    const float *initial;         // [rows][dim][d_state] or nullptr (zero)
+    float *final;                 // [rows][dim][d_state] or nullptr
+    const int32_t *slot_idx, *has_initial;
+    int max_slots;
+    void *y;                      // [T][dim]
+    float *saved;                 // [saved_rows][dim][d_state] or nullptr
+    int *status_dev;
+    // Long sequences on few channels: the token stream cut into `ranges`
+    // ranges of `span` tokens; their local end states and sums of dt
+    // ([ranges][dim][d_state] and [ranges][dim]), and copies of the initial
+    // states of sequences that cross a cut ([ranges][dim][d_state]).
+    // ranges == 0: not cut.
+    int ranges, span;
+    float *range_state, *range_initial, *range_dt;
+};
+// States are saved for the backward pass every kSavedEvery tokens of a
+// sequence, its start included: rows save_row(..) + i of [rows][dim][N].
+// Sequence s starts at row lo / kSavedEvery + s: floor(hi / K) - floor(lo / K)
+// + 1 >= ceil((hi - lo) / K), so sequences never share a row.
+constexpr int kSavedEvery = 32;
+inline long saved_rows(long T, int nseq) { return T / kSavedEvery + nseq; }
+
+struct SelScanBwdArgs {
+    SelScanArgs f;                // the forward call's inputs (y, final unused)
+    const void *dy;               // [T][dim], in_dtype
+    long dy_stride;
+    const float *dfinal;          // [nseq][dim][d_state] or nullptr
+    void *dx, *ddt, *dB, *dC, *dz;
+    float *dA, *dD, *ddt_bias, *dinitial;   // dD, ddt_bias, dinitial may be nullptr
+    // partial sums: per channel tile of a group, and per sequence
+    float *part_B, *part_C;       // [tiles][T][ngroups][d_state]
+    float *part_A;                // [nseq][dim][d_state]
+    float *part_D, *part_bias;    // [nseq][dim]
+};
+int selective_scan_ranges(int nseq, long T, int dim, int d_state, int ngroups, int *span);
+cudaError_t launch_selective_scan(const SelScanArgs &a, cudaStream_t stream);
+size_t selective_scan_bwd_workspace(int nseq, long T, int dim, int d_state, int ngroups);
+cudaError_t launch_selective_scan_bwd(SelScanBwdArgs a, void *workspace, cudaStream_t stream);
+
+// One token per batch row of the per-channel selective scan, in place.
+struct SelUpdateArgs {
+    int batch, dim, d_state, ngroups;
+    int in_bf16, dt_bf16, y_bf16;
+    float *state;                 // [rows][dim][d_state]
+    const int32_t *slot_idx;      // device [batch] or nullptr; < 0 = padding
+    int max_slots;
+    const void *x, *dt, *B, *C, *z;
+    long x_stride, dt_stride, B_stride, C_stride, z_stride;
+    const float *A, *D;
+    DtParams dtp;
+    void *y;                      // [batch][dim]
+    int *status_dev;
+};
+cudaError_t launch_selective_update(const SelUpdateArgs &a, cudaStream_t stream);
+
+// Gradient of the causal conv1d.
+struct ConvBwdArgs {
+    int nseq, seqlen;
+    const int32_t *cu_seqlens;
+    int dim, width, activation, in_bf16;
+    const void *x, *dy;           // [T][dim]
+    const float *weight, *bias;
+    const void *initial;          // [nseq][dim][width-1] or nullptr (zero history)
+    const void *dfinal;           // [nseq][dim][width-1] or nullptr
+    void *dx;                     // [T][dim]
+    float *dweight, *dbias;       // [dim][width], [dim] (nullptr: not wanted)
+    void *dinitial;               // [nseq][dim][width-1] or nullptr
+    float *part;                  // [tiles][width + 1][dim]
+    int *status_dev;
+};
+size_t conv1d_bwd_workspace(long T, int dim, int width);
+cudaError_t launch_conv1d_bwd(const ConvBwdArgs &a, cudaStream_t stream);
+
+// Rows of state pools: pool p's row i is row_bytes bytes at base + i * stride.
+struct PoolRows {
+    char *base;
+    long row_bytes, stride;
+};
+struct PoolArgs {
+    int npools;
+    const PoolRows *pools;        // host array
+    int max_slots, n;             // n pairs (copy) or rows (zero)
+    const int32_t *src, *dst;     // copy: pairs in order; zero: dst
+    const int32_t *count;         // device: how many of the n pairs exist (nullptr: n)
+    int *status_dev;
+};
+cudaError_t launch_pool_copy(const PoolArgs &a, cudaStream_t stream);
+cudaError_t launch_pool_zero(const PoolArgs &a, cudaStream_t stream);
+size_t pool_compact_workspace(int max_slots, int nrows);
+cudaError_t launch_pool_compact(const PoolArgs &a, int32_t *table, int nrows, int32_t *live,
+                                void *workspace, cudaStream_t stream);
+
 // General chunked scan on the CUDA cores: any supported shape and dtype.
 cudaError_t launch_scan_simt(const ScanArgs &a, cudaStream_t stream);
 

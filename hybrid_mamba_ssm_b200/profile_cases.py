@@ -6,6 +6,10 @@
     python -m hybrid_mamba_ssm_b200.profile_cases conv --nseq 1 --seqlen 8192
     python -m hybrid_mamba_ssm_b200.profile_cases conv_update --batch 64
     python -m hybrid_mamba_ssm_b200.profile_cases mtp --batch 16 --ntok 4 --mode verify
+    python -m hybrid_mamba_ssm_b200.profile_cases selective --nseq 1 --seqlen 2048 --dim 8192
+    python -m hybrid_mamba_ssm_b200.profile_cases selective_bwd --nseq 1 --seqlen 2048
+    python -m hybrid_mamba_ssm_b200.profile_cases selective_update --batch 256
+    python -m hybrid_mamba_ssm_b200.profile_cases conv_bwd --seqlen 8192 --dim 10240
 
 Each case draws seeded inputs, runs ``--warmup`` untimed launches and then
 ``--launches`` more, and prints the device time of the last ones.  Inputs are
@@ -101,7 +105,51 @@ def mtp(args, dev):
     return lambda: ssm.ssm_state_update_multi(state, x, dt, A, Bt, Ct, D, y=y)
 
 
-CASES = {"mtp": mtp, "prefill": prefill, "decode": decode, "conv": conv, "conv_update": conv_update}
+def _selective(args, dev, tokens):
+    """Random inputs of the per-channel scan: bf16 activations, a gate, raw dt."""
+    g = torch.Generator(device=dev).manual_seed(86)
+
+    def normal(*shape, scale=1.0, dtype=torch.bfloat16):
+        return (torch.randn(*shape, generator=g, device=dev) * scale).to(dtype)
+
+    dim, N, G = args.dim, args.d_state, args.groups
+    x, z, dt = normal(tokens, dim), normal(tokens, dim), normal(tokens, dim, scale=0.5)
+    B, C = normal(tokens, G, N), normal(tokens, G, N)
+    A = -torch.arange(1, N + 1, device=dev, dtype=torch.float32).repeat(dim, 1)
+    D, bias = normal(dim, dtype=torch.float32), normal(dim, dtype=torch.float32) - 4.0
+    return x, dt, A, B, C, dict(D=D, z=z, dt_bias=bias, dt_softplus=True)
+
+
+def selective(args, dev):
+    x, dt, A, B, C, kw = _selective(args, dev, args.nseq * args.seqlen)
+    kw["cu_seqlens"] = torch.arange(args.nseq + 1, dtype=torch.int32, device=dev) * args.seqlen
+    return lambda: ssm.selective_scan_fwd(x, dt, A, B, C, **kw)
+
+
+def selective_bwd(args, dev):
+    x, dt, A, B, C, kw = _selective(args, dev, args.nseq * args.seqlen)
+    kw["cu_seqlens"] = torch.arange(args.nseq + 1, dtype=torch.int32, device=dev) * args.seqlen
+    saved = ssm.selective_scan_fwd(x, dt, A, B, C, save_states=True, **kw)[2]
+    dy = torch.randn_like(x)
+    return lambda: ssm.selective_scan_bwd(dy, x, dt, A, B, C, saved, **kw)
+
+
+def selective_update(args, dev):
+    x, dt, A, B, C, kw = _selective(args, dev, args.batch)
+    state = torch.zeros((args.batch, args.dim, args.d_state), dtype=torch.float32, device=dev)
+    y = torch.empty_like(x)
+    return lambda: ssm.selective_state_update(state, x, dt, A, B, C, y=y, **kw)
+
+
+def conv_bwd(args, dev):
+    x = torch.randn((args.nseq, args.seqlen, args.dim), device=dev).bfloat16()
+    dy = torch.randn_like(x)
+    w, b = torch.randn((args.dim, args.width), device=dev), torch.randn((args.dim,), device=dev)
+    return lambda: ssm.causal_conv1d_bwd(dy, x, w, b)
+
+
+CASES = {"selective": selective, "selective_bwd": selective_bwd, "selective_update": selective_update,
+         "conv_bwd": conv_bwd, "mtp": mtp, "prefill": prefill, "decode": decode, "conv": conv, "conv_update": conv_update}
 
 
 def main():
@@ -112,8 +160,9 @@ def main():
     ap.add_argument("--batch", type=int, default=16)
     ap.add_argument("--heads", type=int, default=None)
     ap.add_argument("--head-dim", type=int, default=64)
-    ap.add_argument("--d-state", type=int, default=128)
-    ap.add_argument("--groups", type=int, default=8)
+    ap.add_argument("--dim", type=int, default=8192, help="channels (the selective cases, conv_bwd)")
+    ap.add_argument("--d-state", type=int, default=None)
+    ap.add_argument("--groups", type=int, default=None)
     ap.add_argument("--chunk", type=int, default=128)
     ap.add_argument("--width", type=int, default=4)
     ap.add_argument("--ntok", type=int, default=4)
@@ -126,6 +175,11 @@ def main():
     args = ap.parse_args()
     if args.heads is None:
         args.heads = 128 if args.case in ("prefill", "conv") else 256
+    channelwise = args.case.startswith("selective")
+    if args.d_state is None:
+        args.d_state = 16 if channelwise else 128
+    if args.groups is None:
+        args.groups = 1 if channelwise else 8
     dev = torch.device("cuda", 0)
     run = CASES[args.case](args, dev)
     for _ in range(args.warmup):

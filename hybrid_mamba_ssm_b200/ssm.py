@@ -7,8 +7,11 @@ there is no fallback implementation.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
+import math
 import os
+from typing import NamedTuple
 
 import torch
 
@@ -23,7 +26,11 @@ SSM_ERR_TIMEOUT, SSM_ERR_DEVICE_INPUT, SSM_ERR_RANGE = 5, 6, 7
 EXPORTS = ("ssd_chunk_scan", "ssd_chunk_scan_workspace_size", "ssm_state_update",
            "ssd_chunk_scan_slots", "ssm_state_update_slots", "causal_conv1d_fwd",
            "causal_conv1d_update", "ssm_state_update_multi", "ssm_state_commit",
-           "causal_conv1d_update_multi", "ssm_gated_rmsnorm", "ssm_status_string",
+           "causal_conv1d_update_multi", "ssm_gated_rmsnorm", "selective_scan_fwd",
+           "selective_scan_saved_size", "selective_scan_workspace_size", "selective_scan_bwd",
+           "selective_scan_bwd_workspace_size", "selective_state_update", "causal_conv1d_bwd",
+           "causal_conv1d_bwd_workspace_size", "ssm_pool_copy", "ssm_pool_zero", "ssm_pool_compact",
+           "ssm_pool_compact_workspace_size", "ssm_status_string",
            "ssm_version", "ssm_testing_scan_stalled", "ssm_testing_conv1d_stalled")
 ACTIVATIONS = {None: 0, "none": 0, "silu": 1}
 
@@ -66,6 +73,35 @@ def _load():
                                                vp, vp, vp]
     lib.ssm_gated_rmsnorm.restype = i
     lib.ssm_gated_rmsnorm.argtypes = [i, i, i, i, vp, i, vp, vp, ctypes.c_float, i, vp, vp]
+    i64, ll = ctypes.c_int64, ctypes.c_longlong
+    lib.selective_scan_fwd.restype = i
+    lib.selective_scan_fwd.argtypes = [i, i, vp, i, i, i, i, vp, i64, i, vp, i64, vp, vp, i64, vp, i64,
+                                       vp, vp, i64, vp, vp, vp, i, vp, vp, i, vp, vp, vp, sz, vp, vp]
+    lib.selective_scan_saved_size.restype = sz
+    lib.selective_scan_saved_size.argtypes = [i, ll, i, i]
+    lib.selective_scan_workspace_size.restype = sz
+    lib.selective_scan_workspace_size.argtypes = [i, ll, i, i, i]
+    lib.selective_scan_bwd.restype = i
+    lib.selective_scan_bwd.argtypes = [i, i, vp, i, i, i, i, vp, i64, vp, i64, i, vp, i64, vp, vp, i64,
+                                       vp, i64, vp, vp, i64, vp, vp, vp] + [vp] * 10 + [sz, vp, vp]
+    lib.selective_scan_bwd_workspace_size.restype = sz
+    lib.selective_scan_bwd_workspace_size.argtypes = [i, ll, i, i, i]
+    lib.selective_state_update.restype = i
+    lib.selective_state_update.argtypes = [i, i, i, i, vp, i, vp, i, vp, i64, i, vp, i64, vp, vp, i64,
+                                           vp, i64, vp, vp, i64, vp, i, vp, vp, vp]
+    lib.causal_conv1d_bwd.restype = i
+    lib.causal_conv1d_bwd.argtypes = [i, i, vp, i, i, i, vp, vp, vp, vp, i, vp, vp, vp, vp, vp, vp, vp, sz,
+                                      vp, vp]
+    lib.causal_conv1d_bwd_workspace_size.restype = sz
+    lib.causal_conv1d_bwd_workspace_size.argtypes = [ll, i, i]
+    lib.ssm_pool_copy.restype = i
+    lib.ssm_pool_copy.argtypes = [i, vp, i, i, vp, vp, vp, vp]
+    lib.ssm_pool_zero.restype = i
+    lib.ssm_pool_zero.argtypes = [i, vp, i, i, vp, vp, vp]
+    lib.ssm_pool_compact.restype = i
+    lib.ssm_pool_compact.argtypes = [i, vp, i, i, vp, vp, vp, sz, vp, vp]
+    lib.ssm_pool_compact_workspace_size.restype = sz
+    lib.ssm_pool_compact_workspace_size.argtypes = [i, i]
     lib.ssm_status_string.restype = ctypes.c_char_p
     lib.ssm_status_string.argtypes = [i]
     lib.ssm_version.restype = i
@@ -565,6 +601,369 @@ def ssm_gated_rmsnorm(y, z, weight, group_size: int, eps: float = 1e-5, out=None
                                _dtype_code(out.dtype), _ptr(out), _stream(stream))
     _check(st, "ssm_gated_rmsnorm")
     return out
+
+
+# ---------------------------------------------------------------------------
+# Per-channel selective scan, its gradient and decode update, the conv1d
+# gradient, and the rows of state pools.
+# ---------------------------------------------------------------------------
+@contextlib.contextmanager
+def _enter(device, stream):
+    with torch.cuda.device(device), torch.cuda.stream(stream):
+        yield
+
+
+_NO_SCOPE = contextlib.nullcontext()
+
+
+def _scope(t, stream):
+    """The device of t and the given stream made current, so that what a call
+    allocates belongs to the stream that uses it."""
+    if not t.is_cuda:
+        raise ValueError("tensors must be CUDA tensors")
+    if stream is None and t.device.index == torch.cuda.current_device():
+        return _NO_SCOPE
+    return _enter(t.device, stream)
+
+
+def _dev_like(t, name, like, dtype=None, shape=None):
+    """_dev, and t on like's device, of the given shape."""
+    if t is None:
+        return
+    _dev(t, name, dtype)
+    if t.device != like.device:
+        raise ValueError(f"{name} is on {t.device}, not {like.device}")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def _token_rows(t, name, lead, width, like, dtype):
+    """Elements between the tokens of an activation whose leading axes are
+    ``lead`` ([T], or [nseq, L]) and whose trailing axes make a row of
+    ``width`` adjacent elements."""
+    if not t.is_cuda or t.device != like.device:
+        raise ValueError(f"{name} must be a CUDA tensor on {like.device}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    shape, strides = t.shape, t.stride()
+    k = len(lead)
+    if tuple(shape[:k]) != tuple(lead) or math.prod(shape[k:]) != width:
+        raise ValueError(f"{name} must have shape {tuple(lead)} + rows of {width}, got {tuple(shape)}")
+    step = 1
+    for size, stride in zip(reversed(shape[k:]), reversed(strides[k:])):
+        if size > 1 and stride != step:
+            raise ValueError(f"the rows of {name} must be contiguous")
+        step *= size
+    if k == 1:
+        return strides[0] if shape[0] > 1 else width
+    n, length = lead
+    token = strides[1] if length > 1 else (strides[0] if n > 1 else width)
+    if n > 1 and length > 1 and strides[0] != length * token:
+        raise ValueError(f"the tokens of {name} must be equally spaced")
+    return token
+
+
+def _scan_lead(x, cu_seqlens):
+    """(leading axes, nseq, seqlen, tokens, dim) of an x [nseq, L, dim] or packed [T, dim]."""
+    if cu_seqlens is not None:
+        _dev_like(cu_seqlens, "cu_seqlens", x, torch.int32)
+        if x.dim() != 2 or cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 1:
+            raise ValueError("packed x must be [T, dim] with cu_seqlens [nseq+1]")
+        T, dim = x.shape
+        return (T,), cu_seqlens.shape[0] - 1, T, T, dim
+    if x.dim() != 3:
+        raise ValueError("x must be [nseq, L, dim], or [T, dim] with cu_seqlens")
+    n, length, dim = x.shape
+    return (n, length), n, length, n * length, dim
+
+
+def _scan_operands(lead, dim, x, dt, A, B, C, D, z, dt_bias):
+    """Checks the operands of a per-channel scan; their token strides."""
+    in_code, dt_code = _dtype_code(x.dtype), _dtype_code(dt.dtype)
+    if A.dim() != 2 or B.dim() != len(lead) + 2:
+        raise ValueError("A must be [dim, d_state], B and C the tokens' [ngroups, d_state]")
+    N, G = A.shape[1], B.shape[-2]
+    _dev_like(A, "A", x, torch.float32, (dim, N))
+    _dev_like(D, "D", x, torch.float32, (dim,))
+    _dev_like(dt_bias, "dt_bias", x, torch.float32, (dim,))
+    if tuple(B.shape[-2:]) != (G, N) or tuple(C.shape[-2:]) != (G, N):
+        raise ValueError(f"B and C must be [..., {G}, {N}]")
+    xs = _token_rows(x, "x", lead, dim, x, x.dtype)
+    dts = _token_rows(dt, "dt", lead, dim, x, dt.dtype)
+    Bs = _token_rows(B, "B", lead, G * N, x, x.dtype)
+    Cs = _token_rows(C, "C", lead, G * N, x, x.dtype)
+    zs = 0 if z is None else _token_rows(z, "z", lead, dim, x, x.dtype)
+    return in_code, dt_code, N, G, xs, dts, Bs, Cs, zs
+
+
+def _bytes(t) -> int:
+    return 0 if t is None else t.numel() * t.element_size()
+
+
+def _workspace(workspace, size, like):
+    """"auto": a workspace of `size()` bytes (None where that is 0); else what was given."""
+    if isinstance(workspace, str):
+        if workspace != "auto":
+            raise ValueError('workspace must be a CUDA tensor, None or "auto"')
+        n = size()
+        return torch.empty(n, dtype=torch.uint8, device=like.device) if n else None
+    _dev_like(workspace, "workspace", like)
+    return workspace
+
+
+def selective_scan_fwd(x, dt, A, B, C, D=None, z=None, initial_state=None, cu_seqlens=None,
+                       final_state=None, slot_idx=None, has_initial_state=None, dt_bias=None,
+                       dt_softplus=False, dt_limit=None, y=None, y_dtype=None,
+                       return_final_state: bool = True, save_states: bool = False, status=None,
+                       stream=None, workspace="auto"):
+    """Per-channel selective scan over whole sequences.
+
+    x, dt, z : [nseq, L, dim] or, with cu_seqlens (int32 [nseq+1]), packed
+        [T, dim]; x and z bf16 or fp32, dt x's type or fp32; z (the gate) may
+        be None.  Views whose rows are contiguous are taken as they are.
+    A : [dim, d_state] fp32;  D, dt_bias : [dim] fp32 or None
+    B, C : [nseq, L, G, d_state] or [T, G, d_state], x's dtype
+    dt_bias, dt_softplus, dt_limit (lo, hi): dt <- clamp(softplus(dt + dt_bias))
+    initial_state, final_state : [nseq, dim, d_state] fp32, or with slot_idx
+        (int32 [nseq]) a pool [max_slots, dim, d_state]; they may be the same
+        tensor.  has_initial_state : int32 [nseq], 0 starts from zero.
+    save_states : also return what selective_scan_bwd needs of this call.
+    workspace : as for ssd_chunk_scan; lets a long sequence on few channels
+        run in concurrent ranges.
+    Returns (y, final_state), or (y, final_state, saved) with save_states.
+    """
+    with _scope(x, stream):
+        lead, nseq, seqlen, T, dim = _scan_lead(x, cu_seqlens)
+        in_code, dt_code, N, G, xs, dts, Bs, Cs, zs = _scan_operands(lead, dim, x, dt, A, B, C, D, z, dt_bias)
+        pool = nseq
+        if slot_idx is not None:
+            _dev_like(slot_idx, "slot_idx", x, torch.int32, (nseq,))
+            states = final_state if final_state is not None else initial_state
+            if states is None:
+                raise ValueError("slot_idx needs a state pool")
+            pool = states.shape[0]
+        _dev_like(has_initial_state, "has_initial_state", x, torch.int32, (nseq,))
+        _dev_like(initial_state, "initial_state", x, torch.float32, (pool, dim, N))
+        if final_state is None and return_final_state and slot_idx is None:
+            final_state = torch.empty((nseq, dim, N), dtype=torch.float32, device=x.device)
+        _dev_like(final_state, "final_state", x, torch.float32, (pool, dim, N))
+        _dev_like(status, "status", x, torch.int32)
+        if y is None:
+            y = torch.empty(x.shape, dtype=y_dtype or x.dtype, device=x.device)
+        _dev_like(y, "y", x, y_dtype, x.shape)
+        saved = None
+        if save_states:
+            saved = torch.empty(selective_scan_saved_size(nseq, T, dim, N) // 4, dtype=torch.float32,
+                                device=x.device)
+        workspace = None if save_states else _workspace(
+            workspace, lambda: lib.selective_scan_workspace_size(nseq, T, dim, N, G), x)
+        st = lib.selective_scan_fwd(nseq, seqlen, _ptr(cu_seqlens), dim, N, G, in_code, _ptr(x), xs,
+                                    dt_code, _ptr(dt), dts, _ptr(A), _ptr(B), Bs, _ptr(C), Cs, _ptr(D),
+                                    _ptr(z), zs, _dt_params(dt_bias, dt_softplus, dt_limit),
+                                    _ptr(initial_state), _ptr(final_state), pool, _ptr(slot_idx),
+                                    _ptr(has_initial_state), _dtype_code(y.dtype), _ptr(y), _ptr(saved),
+                                    _ptr(workspace), _bytes(workspace), _ptr(status), _stream(None))
+    _check(st, "selective_scan_fwd")
+    return (y, final_state, saved) if save_states else (y, final_state)
+
+
+def selective_scan_saved_size(nseq, ntokens, dim, d_state) -> int:
+    """Bytes that selective_scan_fwd(save_states=True) keeps for the backward pass."""
+    return int(lib.selective_scan_saved_size(nseq, ntokens, dim, d_state))
+
+
+def selective_scan_workspace_size(nseq, ntokens, dim, d_state, ngroups=1) -> int:
+    """Bytes of optional workspace selective_scan_fwd can use for these sizes; 0 if none."""
+    return int(lib.selective_scan_workspace_size(nseq, ntokens, dim, d_state, ngroups))
+
+
+class SelectiveScanGrads(NamedTuple):
+    """Gradients of selective_scan_fwd; None where the input was not given (or,
+    dinitial_state, not asked for)."""
+    dx: torch.Tensor
+    ddt: torch.Tensor
+    dA: torch.Tensor
+    dB: torch.Tensor
+    dC: torch.Tensor
+    dD: torch.Tensor | None
+    dz: torch.Tensor | None
+    ddt_bias: torch.Tensor | None
+    dinitial_state: torch.Tensor | None
+
+
+def selective_scan_bwd(dy, x, dt, A, B, C, saved, D=None, z=None, dfinal_state=None, cu_seqlens=None,
+                       dt_bias=None, dt_softplus=False, dt_limit=None, want_dinitial: bool = False,
+                       status=None, stream=None, workspace="auto") -> SelectiveScanGrads:
+    """Gradient of selective_scan_fwd called with the same inputs and
+    save_states=True (`saved` is its third result).  dy : like x.
+    dfinal_state : [nseq, dim, d_state] fp32 or None.  The gradients have their
+    inputs' shapes and types (contiguous)."""
+    with _scope(x, stream):
+        lead, nseq, seqlen, T, dim = _scan_lead(x, cu_seqlens)
+        in_code, dt_code, N, G, xs, dts, Bs, Cs, zs = _scan_operands(lead, dim, x, dt, A, B, C, D, z, dt_bias)
+        dys = _token_rows(dy, "dy", lead, dim, x, x.dtype)
+        _dev_like(saved, "saved", x, torch.float32)
+        if _bytes(saved) != selective_scan_saved_size(nseq, T, dim, N):
+            raise ValueError("saved is not that of a forward call of these sizes")
+        _dev_like(dfinal_state, "dfinal_state", x, torch.float32, (nseq, dim, N))
+        _dev_like(status, "status", x, torch.int32)
+
+        # a batch of no sequences launches nothing: its sums are zero
+        empty = torch.zeros if nseq == 0 else torch.empty
+
+        def new(shape, dtype=torch.float32):
+            return empty(shape, dtype=dtype, device=x.device)
+
+        g = SelectiveScanGrads(
+            new(x.shape, x.dtype), new(dt.shape, dt.dtype), new((dim, N)), new(B.shape, x.dtype),
+            new(C.shape, x.dtype), None if D is None else new((dim,)),
+            None if z is None else new(z.shape, x.dtype), None if dt_bias is None else new((dim,)),
+            new((nseq, dim, N)) if want_dinitial else None)
+        workspace = _workspace(workspace, lambda: lib.selective_scan_bwd_workspace_size(nseq, T, dim, N, G), x)
+        st = lib.selective_scan_bwd(nseq, seqlen, _ptr(cu_seqlens), dim, N, G, in_code, _ptr(dy), dys,
+                                    _ptr(x), xs, dt_code, _ptr(dt), dts, _ptr(A), _ptr(B), Bs, _ptr(C), Cs,
+                                    _ptr(D), _ptr(z), zs, _dt_params(dt_bias, dt_softplus, dt_limit),
+                                    _ptr(saved), _ptr(dfinal_state), _ptr(g.dx), _ptr(g.ddt), _ptr(g.dA),
+                                    _ptr(g.dB), _ptr(g.dC), _ptr(g.dD), _ptr(g.dz), _ptr(g.ddt_bias),
+                                    _ptr(g.dinitial_state), _ptr(workspace), _bytes(workspace),
+                                    _ptr(status), _stream(None))
+    _check(st, "selective_scan_bwd")
+    return g
+
+
+def selective_scan_bwd_workspace_size(nseq, ntokens, dim, d_state, ngroups=1) -> int:
+    """Bytes of workspace selective_scan_bwd needs for these sizes."""
+    return int(lib.selective_scan_bwd_workspace_size(nseq, ntokens, dim, d_state, ngroups))
+
+
+def selective_state_update(state, x, dt, A, B, C, D=None, z=None, slot_idx=None, dt_bias=None,
+                           dt_softplus=False, dt_limit=None, y=None, y_dtype=None, status=None,
+                           stream=None):
+    """One token per batch row of the per-channel selective scan, in place on
+    ``state`` [batch, dim, d_state] fp32, or on rows slot_idx (int32 [batch],
+    negative: padding row) of a pool [max_slots, dim, d_state].
+
+    x, dt, z : [batch, dim];  B, C : [batch, G, d_state];  A, D, dt_bias and the
+    dt transform as for selective_scan_fwd.  Returns y [batch, dim] (padding
+    rows left as they were)."""
+    with _scope(x, stream):
+        if x.dim() != 2:
+            raise ValueError("x must be [batch, dim]")
+        batch, dim = x.shape
+        in_code, dt_code, N, G, xs, dts, Bs, Cs, zs = _scan_operands((batch,), dim, x, dt, A, B, C, D, z, dt_bias)
+        _dev_like(slot_idx, "slot_idx", x, torch.int32, (batch,))
+        rows = batch if slot_idx is None else state.shape[0]
+        _dev_like(state, "state", x, torch.float32, (rows, dim, N))
+        _dev_like(status, "status", x, torch.int32)
+        if y is None:
+            y = torch.zeros((batch, dim), dtype=y_dtype or x.dtype, device=x.device)
+        _dev_like(y, "y", x, y_dtype, (batch, dim))
+        st = lib.selective_state_update(batch, dim, N, G, _ptr(state), rows, _ptr(slot_idx), in_code,
+                                        _ptr(x), xs, dt_code, _ptr(dt), dts, _ptr(A), _ptr(B), Bs, _ptr(C),
+                                        Cs, _ptr(D), _ptr(z), zs, _dt_params(dt_bias, dt_softplus, dt_limit),
+                                        _dtype_code(y.dtype), _ptr(y), _ptr(status), _stream(None))
+    _check(st, "selective_state_update")
+    return y
+
+
+def causal_conv1d_bwd(dy, x, weight, bias=None, initial_state=None, dfinal_state=None, cu_seqlens=None,
+                      activation="silu", status=None, stream=None, workspace="auto"):
+    """Gradient of causal_conv1d_fwd.  dy, x : [nseq, L, dim] or packed [T, dim]
+    (bf16 or fp32); weight [dim, width], bias [dim] fp32.  initial_state : the
+    conv states before the forward call [nseq, dim, width-1] (it overwrites
+    its conv_state), or None; dfinal_state : gradient of the states it left, or
+    None.  Returns (dx, dweight, dbias, dinitial_state); dbias is None without
+    bias, dinitial_state None without initial_state."""
+    with _scope(x, stream):
+        _dev(x, "x")
+        in_code = _dtype_code(x.dtype)
+        _, nseq, seqlen, T, dim = _scan_lead(x, cu_seqlens)
+        if weight.dim() != 2:
+            raise ValueError("weight must be [dim, width]")
+        width = weight.shape[1]
+        _dev_like(dy, "dy", x, x.dtype, x.shape)
+        _dev_like(weight, "weight", x, torch.float32, (dim, width))
+        _dev_like(bias, "bias", x, torch.float32, (dim,))
+        _dev_like(initial_state, "initial_state", x, x.dtype, (nseq, dim, width - 1))
+        _dev_like(dfinal_state, "dfinal_state", x, x.dtype, (nseq, dim, width - 1))
+        _dev_like(status, "status", x, torch.int32)
+        dx, dweight = torch.empty_like(x), torch.empty_like(weight)
+        dbias = None if bias is None else torch.empty_like(bias)
+        dinitial = None if initial_state is None else torch.empty_like(initial_state)
+        workspace = _workspace(workspace, lambda: lib.causal_conv1d_bwd_workspace_size(T, dim, width), x)
+        st = lib.causal_conv1d_bwd(nseq, seqlen, _ptr(cu_seqlens), dim, width, in_code, _ptr(dy), _ptr(x),
+                                   _ptr(weight), _ptr(bias), _activation(activation), _ptr(initial_state),
+                                   _ptr(dfinal_state), _ptr(dx), _ptr(dweight), _ptr(dbias), _ptr(dinitial),
+                                   _ptr(workspace), _bytes(workspace), _ptr(status), _stream(None))
+    _check(st, "causal_conv1d_bwd")
+    return dx, dweight, dbias, dinitial
+
+
+class Pool(ctypes.Structure):
+    """ssm_pool: row i is row_bytes bytes at base + i * row_stride."""
+    _fields_ = [("base", ctypes.c_void_p), ("row_bytes", ctypes.c_int64), ("row_stride", ctypes.c_int64)]
+
+
+def _pools(pools):
+    """(ssm_pool array, count, max_slots, a tensor of them) of tensors [max_slots, ...]
+    whose rows are contiguous."""
+    pools = [pools] if isinstance(pools, torch.Tensor) else list(pools)
+    if not pools:
+        raise ValueError("no pools given")
+    first, arr = pools[0], (Pool * len(pools))()
+    for k, p in enumerate(pools):
+        if not p.is_cuda or p.device != first.device:
+            raise ValueError("pools must be CUDA tensors on one device")
+        if p.dim() < 1 or p.shape[0] != first.shape[0]:
+            raise ValueError("pools must have the same number of slots")
+        row = p.select(0, 0) if p.shape[0] else p
+        if not row.is_contiguous():
+            raise ValueError("the rows of a pool must be contiguous")
+        nbytes = row.numel() * p.element_size()
+        arr[k] = Pool(p.data_ptr(), nbytes, p.stride(0) * p.element_size() if p.shape[0] > 1 else nbytes)
+    return arr, len(pools), first.shape[0], first
+
+
+def ssm_pool_copy(pools, src_idx, dst_idx, status=None, stream=None) -> None:
+    """Rows dst_idx[i] <- src_idx[i] of every pool, for i in order (a fork copies
+    one row to several).  pools : one tensor or a list of tensors [max_slots,
+    ...] with contiguous rows (any types); src_idx, dst_idx : int32 [n], an
+    entry with a negative index is skipped."""
+    arr, n, slots, like = _pools(pools)
+    with _scope(like, stream):
+        _dev_like(src_idx, "src_idx", like, torch.int32)
+        _dev_like(dst_idx, "dst_idx", like, torch.int32, src_idx.shape)
+        _dev_like(status, "status", like, torch.int32)
+        st = lib.ssm_pool_copy(n, arr, slots, src_idx.numel(), _ptr(src_idx), _ptr(dst_idx), _ptr(status),
+                               _stream(None))
+    _check(st, "ssm_pool_copy")
+
+
+def ssm_pool_zero(pools, row_idx, status=None, stream=None) -> None:
+    """Rows row_idx (int32 [n]; negative: skipped) of every pool <- 0."""
+    arr, n, slots, like = _pools(pools)
+    with _scope(like, stream):
+        _dev_like(row_idx, "row_idx", like, torch.int32)
+        _dev_like(status, "status", like, torch.int32)
+        st = lib.ssm_pool_zero(n, arr, slots, row_idx.numel(), _ptr(row_idx), _ptr(status), _stream(None))
+    _check(st, "ssm_pool_zero")
+
+
+def ssm_pool_compact(pools, slot_idx, status=None, stream=None, workspace="auto"):
+    """Moves the live rows (those that slot_idx, int32 [nrows], names) to the
+    front of every pool and rewrites slot_idx in place.  Returns their number,
+    an int32 scalar tensor."""
+    arr, n, slots, like = _pools(pools)
+    with _scope(like, stream):
+        _dev_like(slot_idx, "slot_idx", like, torch.int32)
+        _dev_like(status, "status", like, torch.int32)
+        live = torch.empty((), dtype=torch.int32, device=like.device)
+        workspace = _workspace(
+            workspace, lambda: lib.ssm_pool_compact_workspace_size(slots, slot_idx.numel()), like)
+        st = lib.ssm_pool_compact(n, arr, slots, slot_idx.numel(), _ptr(slot_idx), _ptr(live),
+                                  _ptr(workspace), _bytes(workspace), _ptr(status), _stream(None))
+    _check(st, "ssm_pool_compact")
+    return live
 
 
 # ---------------------------------------------------------------------------

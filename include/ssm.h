@@ -482,6 +482,196 @@ SSM_API int ssm_gated_rmsnorm(int rows, int dim, int group_size, int y_dtype, co
                               int z_dtype, const void *z, const float *weight, float eps,
                               int out_dtype, void *out, cudaStream_t stream);
 
+/*
+ * Per-channel selective scan.  The scan above has one decay per head; here
+ * every (channel d, state index n) has its own, and the step size is per
+ * channel: the recurrence of the deep-research note, section "1. Selective
+ * SSM 的直觉", with A a [dim][d_state] matrix (the diagonal A of the first
+ * selective state-space models, whose mixers hybrid stacks also use).  For
+ * every sequence, channel d (group g = d / (dim / ngroups)), state index n and
+ * token t in order:
+ *
+ *     v       = dt[t][d] after the optional transform (ssm_dt_params with
+ *               dt_bias [dim], indexed by channel)
+ *     h[d][n] <- exp(v * A[d][n]) * h[d][n] + v * x[t][d] * B[t][g][n]
+ *     y[t][d]  = (sum_n h[d][n] * C[t][g][n] + D[d] * x[t][d]) * silu(z[t][d])
+ *
+ * with silu(z) = z * sigmoid(z), or without that factor when z is NULL.
+ *
+ * Layouts: x, dt, z [T][dim], B, C [T][ngroups][d_state], each with its own
+ * distance between tokens (`*_stride`, in elements, at least the row's
+ * length), so that the halves of an input projection or the slices of a
+ * low-rank projection are passed as they are.  These five (and dy below) need
+ * only the alignment of their element; every other pointer is 16-byte
+ * aligned.  x, B, C, z have in_dtype, dt has dt_dtype: in_dtype or SSM_F32.
+ * A [dim][d_state], D [dim] and the states [rows][dim][d_state] are fp32.
+ * y and the gradients are contiguous.
+ *
+ * All arithmetic is fp32; y and the gradients are rounded once.  d_state in
+ * [1, 256], any dim that ngroups divides.  The method's domain is A <= 0,
+ * v >= 0 (decays at most 1).
+ */
+
+/*
+ * selective_scan_fwd -- whole sequences (nseq, seqlen, cu_seqlens as for
+ * ssd_chunk_scan).
+ *   initial_state / final_state  [rows][dim][d_state] or NULL (zero / not
+ *                written); rows = nseq, or max_slots with slot_idx.  They may
+ *                be the same buffer (a state pool updated in place); any
+ *                other overlap is rejected.
+ *   slot_idx / has_initial_state as for ssd_chunk_scan_slots: device int32
+ *                [nseq] or NULL; distinct rows; an index outside
+ *                [0, max_slots) skips that sequence (y not written) and sets
+ *                SSM_ERR_DEVICE_INPUT.
+ *   y            [T][dim], y_dtype.
+ *   saved_states NULL, or fp32 scratch of selective_scan_saved_size(...)
+ *                bytes that this call fills for selective_scan_bwd: the state
+ *                in front of every 32nd token of a sequence.
+ *   workspace / workspace_bytes  optional scratch of
+ *                selective_scan_workspace_size(...) bytes, or NULL / 0.  With
+ *                it, and without saved_states, a long token stream on few
+ *                channels is cut into ranges that run concurrently (two
+ *                launches); the states that cross a cut are joined in fp32, so
+ *                results agree to rounding.  Calls that share a workspace
+ *                must not overlap on the GPU.
+ */
+SSM_API int selective_scan_fwd(int nseq, int seqlen, const int32_t *cu_seqlens, int dim,
+                               int d_state, int ngroups, int in_dtype,
+                               const void *x, int64_t x_stride,
+                               int dt_dtype, const void *dt, int64_t dt_stride, const float *A,
+                               const void *B, int64_t B_stride, const void *C, int64_t C_stride,
+                               const float *D, const void *z, int64_t z_stride,
+                               const ssm_dt_params *dt_params, const float *initial_state,
+                               float *final_state, int max_slots, const int32_t *slot_idx,
+                               const int32_t *has_initial_state, int y_dtype, void *y,
+                               float *saved_states, void *workspace, size_t workspace_bytes,
+                               int *status_dev, cudaStream_t stream);
+
+/* Bytes of saved_states for ntokens tokens in nseq sequences. */
+SSM_API size_t selective_scan_saved_size(int nseq, long long ntokens, int dim, int d_state);
+
+/* Workspace bytes selective_scan_fwd can use for these sizes on the current
+ * device; 0 where the channels alone fill it. */
+SSM_API size_t selective_scan_workspace_size(int nseq, long long ntokens, int dim, int d_state,
+                                             int ngroups);
+
+/*
+ * selective_scan_bwd -- the gradient of selective_scan_fwd (without slots).
+ * Inputs as in the forward call, and
+ *   dy            gradient of y, [T][dim] in in_dtype (dy_stride elements
+ *                 between tokens)
+ *   saved_states  as the forward call filled it
+ *   dfinal_state  gradient of the final states, fp32 [nseq][dim][d_state], or
+ *                 NULL (zero)
+ * Outputs: dx, dB, dC, dz in in_dtype, ddt in dt_dtype (gradient of the raw
+ * dt), dA [dim][d_state], dD [dim] (or NULL), ddt_bias [dim] (or NULL; the sum
+ * of the gradients of the raw dt over the tokens), dinitial_state
+ * [nseq][dim][d_state] (or NULL) in fp32.  dz goes with z.  Every sum is fp32
+ * and in a fixed order: equal calls give equal bits.  Where the clamp of the
+ * step size is active its gradient is zero.
+ *   workspace     selective_scan_bwd_workspace_size(...) bytes, required.
+ * Two launches.
+ */
+SSM_API int selective_scan_bwd(int nseq, int seqlen, const int32_t *cu_seqlens, int dim,
+                               int d_state, int ngroups, int in_dtype,
+                               const void *dy, int64_t dy_stride, const void *x, int64_t x_stride,
+                               int dt_dtype, const void *dt, int64_t dt_stride, const float *A,
+                               const void *B, int64_t B_stride, const void *C, int64_t C_stride,
+                               const float *D, const void *z, int64_t z_stride,
+                               const ssm_dt_params *dt_params, const float *saved_states,
+                               const float *dfinal_state, void *dx, void *ddt, float *dA, void *dB,
+                               void *dC, float *dD, void *dz, float *ddt_bias,
+                               float *dinitial_state, void *workspace, size_t workspace_bytes,
+                               int *status_dev, cudaStream_t stream);
+
+SSM_API size_t selective_scan_bwd_workspace_size(int nseq, long long ntokens, int dim, int d_state,
+                                                 int ngroups);
+
+/*
+ * selective_state_update -- decode: one token per batch row, in place on the
+ * row's state (state[b], or state[slot_idx[b]] of a pool of max_slots rows).
+ * x, dt, z [batch][dim], B, C [batch][ngroups][d_state] with strides as above;
+ * y [batch][dim], y_dtype.  A negative slot marks a padding row (state and y
+ * untouched); an index >= max_slots skips the row and sets
+ * SSM_ERR_DEVICE_INPUT.  Slots of non-padding rows must be distinct.  Each
+ * state element is read once and written once.
+ */
+SSM_API int selective_state_update(int batch, int dim, int d_state, int ngroups, float *state,
+                                   int max_slots, const int32_t *slot_idx, int in_dtype,
+                                   const void *x, int64_t x_stride,
+                                   int dt_dtype, const void *dt, int64_t dt_stride, const float *A,
+                                   const void *B, int64_t B_stride, const void *C, int64_t C_stride,
+                                   const float *D, const void *z, int64_t z_stride,
+                                   const ssm_dt_params *dt_params, int y_dtype, void *y,
+                                   int *status_dev, cudaStream_t stream);
+
+/*
+ * causal_conv1d_bwd -- the gradient of causal_conv1d_fwd.  dy, x, dx [T][dim]
+ * and the conv states [nseq][dim][width-1] are contiguous, in in_dtype.
+ *   initial_state   the conv states before the forward call (which overwrites
+ *                   its conv_state), or NULL (zero history)
+ *   dfinal_state    gradient of the conv states it left (copies of the last
+ *                   width-1 inputs), or NULL (zero)
+ *   dweight [dim][width], dbias [dim] (or NULL): fp32 sums over all tokens, in
+ *                   a fixed order
+ *   dinitial_state  gradient of the history entries, or NULL
+ *   workspace       causal_conv1d_bwd_workspace_size(...) bytes, required
+ * A sequence whose offsets are inconsistent is skipped (SSM_ERR_DEVICE_INPUT).
+ */
+SSM_API int causal_conv1d_bwd(int nseq, int seqlen, const int32_t *cu_seqlens, int dim, int width,
+                              int in_dtype, const void *dy, const void *x, const float *weight,
+                              const float *bias, int activation, const void *initial_state,
+                              const void *dfinal_state, void *dx, float *dweight, float *dbias,
+                              void *dinitial_state, void *workspace, size_t workspace_bytes,
+                              int *status_dev, cudaStream_t stream);
+
+SSM_API size_t causal_conv1d_bwd_workspace_size(long long ntokens, int dim, int width);
+
+/*
+ * Rows of state pools.  A request owns one row (slot) in the recurrent and the
+ * conv pool of every layer; these calls copy, free and compact rows of any
+ * number of pools at once (the slot life cycle of the MAX nemotron_h article,
+ * section 8).  Pool p's row i is row_bytes bytes at base + i * row_stride, for
+ * i in [0, max_slots): an SSM or conv pool of any type or layout whose slots
+ * are contiguous.  Rows must not overlap, in a pool or between pools.  Index
+ * lists are device int32, 16-byte aligned.  A negative index skips its entry;
+ * one >= max_slots skips it and sets SSM_ERR_DEVICE_INPUT.
+ */
+typedef struct {
+    void *base;
+    int64_t row_bytes;
+    int64_t row_stride;   /* bytes, >= row_bytes */
+} ssm_pool;
+
+#define SSM_MAX_POOLS 1024   /* pools of one call (SSM_ERR_UNSUPPORTED beyond) */
+
+/* ssm_pool_copy -- for i = 0 .. npairs-1 in this order: row dst_idx[i] <- row
+ * src_idx[i].  The meaning is that of the loop, whatever rows repeat (several
+ * copies of one row fork a request; a row may be read after it was written). */
+SSM_API int ssm_pool_copy(int npools, const ssm_pool *pools, int max_slots, int npairs,
+                          const int32_t *src_idx, const int32_t *dst_idx, int *status_dev,
+                          cudaStream_t stream);
+
+/* ssm_pool_zero -- rows row_idx[0 .. nrows-1] <- 0 (a freed or claimed slot). */
+SSM_API int ssm_pool_zero(int npools, const ssm_pool *pools, int max_slots, int nrows,
+                          const int32_t *row_idx, int *status_dev, cudaStream_t stream);
+
+/*
+ * ssm_pool_compact -- moves the live rows to the front.  slot_idx (device
+ * int32 [nrows], read and rewritten) names the row of each request; negative
+ * entries are padding and stay.  With n distinct live rows, those at n and
+ * above move, in ascending order, into the free rows below n, in ascending
+ * order; the others stay.  *nlive (device int32, or NULL) receives n.  Rows
+ * that were moved from keep their old contents.  The moves are worked out on
+ * the device: nothing is read back.
+ *   workspace  ssm_pool_compact_workspace_size(max_slots, nrows) bytes
+ */
+SSM_API int ssm_pool_compact(int npools, const ssm_pool *pools, int max_slots, int nrows,
+                             int32_t *slot_idx, int32_t *nlive, void *workspace,
+                             size_t workspace_bytes, int *status_dev, cudaStream_t stream);
+
+SSM_API size_t ssm_pool_compact_workspace_size(int max_slots, int nrows);
+
 #ifdef __cplusplus
 }
 #endif
