@@ -15,6 +15,9 @@ struct Rows {
     int dtype;
 };
 
+// The kernels address a tile of up to 32 tokens by 32-bit offsets.
+constexpr int64_t kMaxRow = 1 << 24;
+
 size_t rows_bytes(const Rows &r, long long T)
 {
     return T > 0 ? (size_t)(((T - 1) * r.stride + r.width) * (long long)dtype_size(r.dtype)) : 0;
@@ -26,9 +29,16 @@ int check_rows(const Rows &r, long long T)
 {
     if (!r.p) return T > 0 ? SSM_ERR_INVALID_ARG : SSM_OK;
     if (T > 1 && r.stride < r.width) return SSM_ERR_INVALID_ARG;
-    if (r.stride < 0 || r.stride > (1LL << 40)) return SSM_ERR_INVALID_ARG;
+    if (r.stride < 0) return SSM_ERR_INVALID_ARG;
+    if (r.stride > kMaxRow || r.width > kMaxRow) return SSM_ERR_UNSUPPORTED;
     if (reinterpret_cast<uintptr_t>(r.p) % dtype_size(r.dtype)) return SSM_ERR_MISALIGNED;
     return SSM_OK;
+}
+
+// Whether channels 2i and 2i + 1 of every token are one aligned access.
+bool paired(const Rows &r)
+{
+    return !r.p || (r.stride % 2 == 0 && reinterpret_cast<uintptr_t>(r.p) % (2 * dtype_size(r.dtype)) == 0);
 }
 
 // No output overlaps an input or another output.
@@ -133,6 +143,7 @@ int selective_scan_fwd(int nseq, int seqlen, const int32_t *cu_seqlens, int dim,
     a.initial = initial_state; a.final = final_state;
     a.slot_idx = slot_idx; a.has_initial = has_initial_state; a.max_slots = max_slots;
     a.y = y; a.saved = saved_states; a.status_dev = status_dev;
+    a.pairs = dim / ngroups % 2 == 0 && paired(rows[0]) && paired(rows[1]) && paired(rows[4]);
     if (cut) {
         a.ranges = ssm::selective_scan_ranges(nseq, T, dim, d_state, ngroups, &a.span);
         const size_t n = up16((size_t)a.ranges * srow * sizeof(float));

@@ -99,26 +99,76 @@ __device__ __forceinline__ int reduce_lanes(float (&v)[TG], int lane) {
     return first;
 }
 
+__device__ __forceinline__ float min_nan(float a, float b) {   // NaN if either is
+    float r;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
+// e^-a for a >= 0 to about an ulp: 2^t with the rounding of t = -a log2 e
+// carried as a first-order correction.
+__device__ __forceinline__ float exp_neg(float a) {
+    const float t = a * -kLog2e, lost = fmaf(a, -kLog2e, -t) - a * 1.9259629911e-8f;
+    const float e = ex2_approx(t);
+    return fmaf(e, lost * kLn2, e);
+}
+
+// log(1 + e^v) = max(v, 0) + log1p(e) with e = e^-|v| in [0, 1]; log1p(e) / e
+// is interpolated at ten Chebyshev nodes of [0, 1] (error 1.4e-8).  A step
+// size enters every decay of its token, so it is kept to about an ulp.
+__device__ constexpr float kLog1p[10] = {
+    1.f, -0.49999892711639404f, 0.33329710364341736f, -0.24951615929603577f, 0.1966327428817749f,
+    -0.1526966691017151f, 0.10543623566627502f, -0.056373611092567444f, 0.019542526453733444f,
+    -0.0031760570127516985f};
+__device__ __forceinline__ float log1p_unit(float e) {
+    float q = kLog1p[9];
+#pragma unroll
+    for (int i = 8; i >= 0; --i) q = fmaf(q, e, kLog1p[i]);
+    return q * e;
+}
+
 // dt after the optional transform, and the derivative of that transform with
-// respect to the raw dt: sigmoid of the biased value for the softplus (1
-// above 20, where log1p(e^v) equals v in fp32), 0 where the clamp is active.
-// expf rather than the faster __expf: a step size enters every decay of its
-// token, so its relative error is felt over the whole memory of a state.
+// respect to the raw dt: the sigmoid of the biased value for the softplus, 0
+// where the clamp is active.  exp_neg's argument is capped where the result
+// has long been 0 (infinities would meet in its correction).
 __device__ __forceinline__ float dt_value(const DtParams &p, float raw, float bias) {
     float v = raw + bias;
-    if (p.softplus) v = v > 20.f ? v : log1pf(expf(v));
+    if (p.softplus) v = fmaxf(v, 0.f) + log1p_unit(exp_neg(min_nan(fabsf(v), 120.f)));
     if (p.clamp) v = fminf(fmaxf(v, p.lo), p.hi);
     return v;
 }
 __device__ __forceinline__ float dt_slope(const DtParams &p, float raw, float bias) {
     float v = raw + bias, d = 1.f;
-    if (p.softplus && v <= 20.f) {
-        const float e = expf(v);
-        d = __fdividef(e, 1.f + e);
-        v = log1pf(e);
+    if (p.softplus) {
+        const float e = exp_neg(min_nan(fabsf(v), 120.f)), r = rcp_approx(1.f + e);
+        d = v >= 0.f ? r : e * r;
+        v = fmaxf(v, 0.f) + log1p_unit(e);
     }
     if (p.clamp && (v < p.lo || v > p.hi)) d = 0.f;
     return d;
+}
+
+// dt_value of two channels at once (packed).
+__device__ __forceinline__ f32x2 dt_value2(const DtParams &p, f32x2 raw, f32x2 bias) {
+    f32x2 v = add2(raw, bias);
+    if (p.softplus) {
+        const f32x2 a = pack2(min_nan(fabsf(lo2(v)), 120.f), min_nan(fabsf(hi2(v)), 120.f));
+        const f32x2 t = mul2(a, pack2(-kLog2e, -kLog2e));
+        const f32x2 lost = fma2(a, pack2(1.9259629911e-8f, 1.9259629911e-8f), fma2(a, pack2(kLog2e, kLog2e), t));
+        f32x2 e = ex2_pair(t);
+        e = fma2(e, mul2(lost, pack2(-kLn2, -kLn2)), e);
+        f32x2 q = pack2(kLog1p[9], kLog1p[9]);
+#pragma unroll
+        for (int i = 8; i >= 0; --i) q = fma2(q, e, pack2(kLog1p[i], kLog1p[i]));
+        v = fma2(q, e, pack2(fmaxf(lo2(v), 0.f), fmaxf(hi2(v), 0.f)));
+    }
+    if (p.clamp)
+        v = pack2(fminf(fmaxf(lo2(v), p.lo), p.hi), fminf(fmaxf(hi2(v), p.lo), p.hi));
+    return v;
+}
+__device__ __forceinline__ f32x2 silu2(f32x2 z) {
+    const f32x2 d = add2(ex2_pair(mul2(z, pack2(-kLog2e, -kLog2e))), pack2(1.f, 1.f));
+    return mul2(z, pack2(rcp_approx(lo2(d)), rcp_approx(hi2(d))));
 }
 
 // An activation value as loaded, and its fp32 value.  Loads keep the raw bits
@@ -131,6 +181,27 @@ __device__ __forceinline__ uint32_t raw_load(const void *p, long i) {
 template <typename T>
 __device__ __forceinline__ float raw_value(uint32_t r) {
     return __uint_as_float(sizeof(T) == 2 ? r << 16 : r);
+}
+// Two adjacent values.  pair_load wants an address aligned to both; either way
+// the registers hold what pair_value takes: a bf16 pair is one register, or
+// two with a value in the low half of each.
+template <typename T>
+__device__ __forceinline__ void pair_load(const T *p, int i, uint32_t (&r)[2]) {
+    if constexpr (sizeof(T) == 2) {
+        r[0] = *reinterpret_cast<const uint32_t *>(p + i);
+        r[1] = 0u;
+    } else {
+        const uint2 q = *reinterpret_cast<const uint2 *>(p + i);
+        r[0] = q.x;
+        r[1] = q.y;
+    }
+}
+template <typename T>
+__device__ __forceinline__ f32x2 pair_value(const uint32_t (&r)[2]) {
+    if constexpr (sizeof(T) == 2)
+        return pack2(__uint_as_float(r[0] << 16), __uint_as_float((r[0] & 0xffff0000u) | (r[1] << 16)));
+    else
+        return pack2(__uint_as_float(r[0]), __uint_as_float(r[1]));
 }
 template <typename T>
 __device__ __forceinline__ float ld_as(const void *p, long i) {

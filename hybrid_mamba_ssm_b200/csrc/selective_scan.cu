@@ -27,16 +27,24 @@ constexpr int kThreads = 128;
 
 constexpr int min3(int a, int b, int c) { return a < b ? (a < c ? a : c) : (b < c ? b : c); }
 
-template <int R, int L>
+template <int R, int L, int Q>
 struct ScanShape {
-    static constexpr int CT = kThreads / L;                      // channels per CTA
+    static constexpr int CS = kThreads / L;                      // channels of a set
+    static constexpr int CT = CS * Q;                            // channels per CTA
     static constexpr int NP = R * L;                             // states, zero padded
-    static constexpr int KT = min3(32, 1024 / NP, 1024 / CT);    // tokens per tile
-    static constexpr int TG = KT < 4 ? KT : 4;                   // tokens summed together
-    static constexpr int RS = kThreads / CT;                     // tokens per staging step
-    static constexpr int E = (KT + RS - 1) / RS;                 // staged values per thread
+    static constexpr int KT = min3(32, 1024 / NP, 512 / CT);     // tokens per tile
+    static constexpr int TG = 4;                                 // tokens per step of the scan
+    static constexpr int RS = kThreads / (CT / 2);               // tokens per staging step (a thread: two channels)
+    static constexpr int E = (KT + RS - 1) / RS;                 // staged pairs per thread
     static constexpr int EB = (KT * NP + kThreads - 1) / kThreads;
+    static constexpr int YP = L < 4 ? L : 4;                     // partial sums over n left to the output step
+    static_assert(KT % TG == 0 && CT % 2 == 0, "");
 };
+
+// CTAs that an SM must hold at once: registers are the limit (a thread keeps
+// 4 R Q of them for the states and decay rates).
+template <int R, int Q>
+constexpr int kMinBlocks = R * Q <= 4 ? 7 : 4;
 
 // States of one channel: R values from index j * R on, zero behind d_state.
 template <int R>
@@ -99,18 +107,19 @@ enum { kWhole = 0, kRangeState = 1, kRangeOut = 2 };
 // exp(A sum v).  It also copies the initial state of a sequence that goes on
 // behind the range.  The second folds the ranges before its own and runs its
 // tokens from the state that enters.
-template <typename TIn, typename TDt, int R, int L, int kMode>
-__global__ void __launch_bounds__(kThreads)
+template <typename TIn, typename TDt, int R, int L, int Q, int kMode>
+__global__ void __launch_bounds__(kThreads, kMinBlocks<R, Q>)
 selective_scan_kernel(SelScanArgs a)
 {
-    using S = ScanShape<R, L>;
-    constexpr int CT = S::CT, NP = S::NP, KT = S::KT, TG = S::TG, RS = S::RS, E = S::E, EB = S::EB;
-    constexpr int P = R / 2;
-    __shared__ __align__(16) float s_v[KT * CT];
-    __shared__ __align__(16) float s_u[KT * CT];
-    __shared__ __align__(16) float s_y[kMode == kRangeState ? 1 : KT * CT];
-    __shared__ __align__(16) float s_B[KT * NP];
-    __shared__ __align__(16) float s_C[kMode == kRangeState ? 4 : KT * NP];
+    using S = ScanShape<R, L, Q>;
+    constexpr int CS = S::CS, CT = S::CT, NP = S::NP, KT = S::KT, TG = S::TG, RS = S::RS, E = S::E, EB = S::EB;
+    constexpr int P = R / 2, YP = S::YP;
+    constexpr bool kOut = kMode != kRangeState;
+    // two buffers each: a tile is staged while the one before is still read
+    __shared__ __align__(16) float2 s_vu[2][KT * CT];            // step size, step size times x
+    __shared__ __align__(16) float s_B[2][KT * NP];
+    __shared__ __align__(16) float s_C[2][kOut ? KT * NP : 4];
+    __shared__ __align__(16) float s_y[2][kOut ? KT * CT * YP : 4];
 
     const int tid = threadIdx.x, lane = tid & 31;
     const int gdim = a.dim / a.ngroups, gtiles = (gdim + CT - 1) / CT, tiles = gtiles * a.ngroups;
@@ -119,126 +128,211 @@ selective_scan_kernel(SelScanArgs a)
     const int N = a.d_state;
     const long T = a.cu_seqlens ? (long)a.seqlen : (long)a.nseq * a.seqlen;
 
-    const int j = tid % L, ch = tid / L, d = c0 + ch;      // scanning: lane j of channel d
-    const int sc = tid % CT, st = tid / CT, ds = c0 + sc;  // staging: channel ds
-    const bool live = d < cend, slive = ds < cend;
-    const float bias = slive && a.dtp.bias ? a.dtp.bias[ds] : 0.f;
-    const float skip = slive && a.D ? a.D[ds] : 0.f;
-
-    f32x2 A[P], h[P];
-#pragma unroll
-    for (int p = 0; p < P; ++p) A[p] = pack2(0.f, 0.f);
-    if (live) load_states<R>(a.A + (long)d * N, j, N, A);
-#pragma unroll
-    for (int p = 0; p < P; ++p) A[p] = mul2(A[p], pack2(kLog2e, kLog2e));
-
-    float vsum = 0.f;
-    uint32_t xr[E], vr[E], Br[EB], Cr[EB];      // raw values of the next tile
-
-    // Raw values of the tile at t (tokens up to te), zero elsewhere.
-    auto fetch = [&](long t, long te) {
-#pragma unroll
-        for (int i = 0; i < E; ++i) {
-            const long tt = t + st + i * RS;
-            const bool ok = slive && tt < te && st + i * RS < KT;
-            xr[i] = ok ? raw_load<TIn>(a.x, tt * a.x_stride + ds) : 0u;
-            vr[i] = ok ? raw_load<TDt>(a.dt, tt * a.dt_stride + ds) : 0u;
-        }
-#pragma unroll
-        for (int i = 0; i < EB; ++i) {
-            const int e = tid + i * kThreads, n = e % NP;
-            const long tt = t + e / NP;
-            const bool ok = n < N && tt < te && e < KT * NP;
-            Br[i] = ok ? raw_load<TIn>(a.B, tt * a.B_stride + (long)g * N + n) : 0u;
-            if (kMode != kRangeState)
-                Cr[i] = ok ? raw_load<TIn>(a.C, tt * a.C_stride + (long)g * N + n) : 0u;
-        }
+    const int j = tid % L, ch = tid / L, d0 = c0 + ch;     // scanning: lane j of channels d0 + q CS
+    const int sc = 2 * (tid % (CT / 2)), st = tid / (CT / 2), ds = c0 + sc;   // staging: channels ds, ds + 1
+    const bool slive0 = ds < cend, slive1 = ds + 1 < cend;
+    auto per_channel = [&](const float *p) {
+        return pack2(p && slive0 ? p[ds] : 0.f, p && slive1 ? p[ds + 1] : 0.f);
     };
+    const f32x2 bias = per_channel(a.dtp.bias), skip = per_channel(a.D);
+    auto live = [&](int q) { return d0 + q * CS < cend; };
+    auto row_of = [&](const float *p, long row, int q) { return p + (row * a.dim + d0 + q * CS) * N; };
 
-    // Tokens [t, te) of a sequence that starts at token lo.
-    auto run = [&](long t, long te, long lo, long save0) {
-        auto tile_end = [&](long t0) {   // tiles end on multiples of KT of the sequence
-            return min(te, t0 + KT - (t0 - lo) % KT);
-        };
-        long t1 = tile_end(t);
-        fetch(t, t1);
-        while (t < te) {
-            float xc[E];
-            uint32_t zc[E];
+    f32x2 A[Q][P], h[Q][P];
+    float vsum[Q];
+#pragma unroll
+    for (int q = 0; q < Q; ++q) {
+        vsum[q] = 0.f;
+#pragma unroll
+        for (int p = 0; p < P; ++p) A[q][p] = pack2(0.f, 0.f);
+        if (live(q)) load_states<R>(row_of(a.A, 0, q), j, N, A[q]);
+#pragma unroll
+        for (int p = 0; p < P; ++p) A[q][p] = mul2(A[q][p], pack2(kLog2e, kLog2e));
+    }
+    // Raw values of the next tile; x and z of the one whose output is due.
+    uint32_t xr[E][2], vr[E][2], zr[E][2], Br[EB], Cr[EB], xc[E][2], zc[E][2];
+
+    // Offsets of this thread's staged values from the tile's first row: 32 bits
+    // (strides are at most 2^24), so that an address is a uniform base plus one.
+    const int xs = (int)a.x_stride, vs = (int)a.dt_stride, Bs = (int)a.B_stride, Cs = (int)a.C_stride, zs = (int)a.z_stride;
+    const int x0 = st * xs + sc, v0 = st * vs + sc, z0 = st * zs + sc, y0 = st * a.dim + sc;
+    const bool whole_rows = a.pairs && cend - c0 == CT && N == NP;   // no channel or state of the tile is padding
+
+    // Raw values of n tokens from t on, zero behind them.
+    auto fetch = [&](long t, int n) {
+        const TIn *xt = static_cast<const TIn *>(a.x) + t * xs + c0;
+        const TIn *zt = static_cast<const TIn *>(a.z) + t * zs + c0;
+        const TDt *vt = static_cast<const TDt *>(a.dt) + t * vs + c0;
+        const TIn *Bt = static_cast<const TIn *>(a.B) + t * Bs + g * N;
+        const TIn *Ct = static_cast<const TIn *>(a.C) + t * Cs + g * N;
+        if (n == KT && whole_rows) {
 #pragma unroll
             for (int i = 0; i < E; ++i) {
-                const int k = st + i * RS;
-                xc[i] = raw_value<TIn>(xr[i]);
-                if (k < KT) {
-                    const float v = slive && t + k < t1 ? dt_value(a.dtp, raw_value<TDt>(vr[i]), bias) : 0.f;
-                    s_v[k * CT + sc] = v;
-                    s_u[k * CT + sc] = v * xc[i];
+                if (KT % RS && st + i * RS >= KT) break;
+                pair_load(xt, x0 + i * RS * xs, xr[i]);
+                pair_load(vt, v0 + i * RS * vs, vr[i]);
+                if (kOut && a.z) pair_load(zt, z0 + i * RS * zs, zr[i]);
+            }
+#pragma unroll
+            for (int i = 0; i < EB; ++i) {
+                const int e = tid + i * kThreads;
+                if (KT * NP % kThreads && e >= KT * NP) break;
+                Br[i] = raw_load<TIn>(Bt, e / NP * Bs + e % NP);
+                if (kOut) Cr[i] = raw_load<TIn>(Ct, e / NP * Cs + e % NP);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < E; ++i) {
+                const bool in = st + i * RS < n;
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    const bool ok = in && (q ? slive1 : slive0);
+                    xr[i][q] = ok ? raw_load<TIn>(xt, x0 + i * RS * xs + q) : 0u;
+                    vr[i][q] = ok ? raw_load<TDt>(vt, v0 + i * RS * vs + q) : 0u;
+                    if (kOut) zr[i][q] = ok && a.z ? raw_load<TIn>(zt, z0 + i * RS * zs + q) : 0u;
                 }
             }
 #pragma unroll
             for (int i = 0; i < EB; ++i) {
                 const int e = tid + i * kThreads;
-                if (e < KT * NP) {
-                    s_B[e] = raw_value<TIn>(Br[i]);
-                    if (kMode != kRangeState) s_C[e] = raw_value<TIn>(Cr[i]);
-                }
+                const bool ok = e % NP < N && e / NP < n;
+                Br[i] = ok ? raw_load<TIn>(Bt, e / NP * Bs + e % NP) : 0u;
+                if (kOut) Cr[i] = ok ? raw_load<TIn>(Ct, e / NP * Cs + e % NP) : 0u;
             }
-            __syncthreads();
-            const long t2 = t1 < te ? tile_end(t1) : t1;
-            if (t1 < te) fetch(t1, t2);
-            if (kMode != kRangeState && a.z) {
+        }
+    };
+    // Step sizes, B and C of the fetched tile of n tokens into buffer b.
+    auto stage = [&](int n, int b) {
 #pragma unroll
-                for (int i = 0; i < E; ++i) {
-                    const int k = st + i * RS;
-                    zc[i] = slive && k < KT && t + k < t1 ? raw_load<TIn>(a.z, (t + k) * a.z_stride + ds) : 0u;
+        for (int i = 0; i < E; ++i) {
+            const int k = st + i * RS;
+            if (KT % RS && k >= KT) break;
+            f32x2 v = dt_value2(a.dtp, pair_value<TDt>(vr[i]), bias);
+            if (k >= n) v = pack2(0.f, 0.f);       // tokens behind the tile leave the state as it is
+            const f32x2 u = mul2(v, pair_value<TIn>(xr[i]));
+            *reinterpret_cast<float4 *>(&s_vu[b][k * CT + sc]) = make_float4(lo2(v), lo2(u), hi2(v), hi2(u));
+        }
+#pragma unroll
+        for (int i = 0; i < EB; ++i) {
+            const int e = tid + i * kThreads;
+            if (KT * NP % kThreads && e >= KT * NP) break;
+            s_B[b][e] = raw_value<TIn>(Br[i]);
+            if (kOut) s_C[b][e] = raw_value<TIn>(Cr[i]);
+        }
+    };
+    // y of a tile of n tokens from t on, from the partial sums of buffer b.
+    auto output = [&](long t, int n, int b) {
+        const long yt = t * a.dim + c0;
+#pragma unroll
+        for (int i = 0; i < E; ++i) {
+            const int k = st + i * RS;
+            if (k >= n || !slive0) break;
+            float f[2];
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                f32x2 part[(YP + 1) / 2];
+                if constexpr (YP == 1) {
+                    f[q] = s_y[b][k * CT + sc + q];
+                } else {
+                    lds_pairs(&s_y[b][(k * CT + sc + q) * YP], part);
+                    f[q] = sum2(YP == 4 ? add2(part[0], part[YP / 2 - 1]) : part[0]);
                 }
             }
-            if (kMode != kRangeState && a.saved && (t - lo) % kSavedEvery == 0 && live)
-                store_states<R>(a.saved + ((save0 + (t - lo) / kSavedEvery) * a.dim + d) * N, j, N, h);
+            f32x2 y = fma2(skip, pair_value<TIn>(xc[i]), pack2(f[0], f[1]));
+            if (a.z) y = mul2(y, silu2(pair_value<TIn>(zc[i])));
+            const int o = y0 + i * RS * a.dim;
+            if (a.y_bf16) {
+                __nv_bfloat16 *yp = static_cast<__nv_bfloat16 *>(a.y) + yt + o;
+                if (slive1 && a.dim % 2 == 0) {
+                    *reinterpret_cast<__nv_bfloat162 *>(yp) = __floats2bfloat162_rn(lo2(y), hi2(y));
+                } else {
+                    store_out(yp, lo2(y));
+                    if (slive1) store_out(yp + 1, hi2(y));
+                }
+            } else {
+                float *yp = static_cast<float *>(a.y) + yt + o;
+                store_out(yp, lo2(y));
+                if (slive1) store_out(yp + 1, hi2(y));
+            }
+        }
+    };
 
+    // Tokens [t, te) of a sequence that starts at token lo.  One barrier per
+    // tile: the output of the tile before and the scan of this one follow it.
+    auto run = [&](long t, long te, long lo, long save0) {
+        int rel = (int)(t - lo), left = (int)(te - t), before = 0, b = 0;
+        int n = min(left, KT - rel % KT);          // tiles end on multiples of KT of the sequence
+        fetch(t, n);
+        while (left > 0) {
+            stage(n, b);
+            __syncthreads();
+            if (kOut) {
+                if (before) output(t - before, before, b ^ 1);
+#pragma unroll
+                for (int i = 0; i < E; ++i)
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        xc[i][q] = xr[i][q];
+                        zc[i][q] = zr[i][q];
+                    }
+            }
+            const int n2 = min(left - n, KT);
+            if (n2 > 0) fetch(t + n, n2);
+            if (kOut && a.saved && rel % kSavedEvery == 0) {
+#pragma unroll
+                for (int q = 0; q < Q; ++q)
+                    if (live(q)) store_states<R>(const_cast<float *>(row_of(a.saved, save0 + rel / kSavedEvery, q)), j, N, h[q]);
+            }
 #pragma unroll 1
-            for (int k0 = 0; k0 < KT && t + k0 < t1; k0 += TG) {
-                float yv[TG];
+            for (int k0 = 0; k0 < n; k0 += TG) {
+                float yv[Q][TG];
 #pragma unroll
                 for (int k = 0; k < TG; ++k) {
-                    const float v = s_v[(k0 + k) * CT + ch], u = s_u[(k0 + k) * CT + ch];
-                    const f32x2 vv = pack2(v, v), uu = pack2(u, u);
-                    f32x2 B[P], C[P], acc = pack2(0.f, 0.f);
-                    lds_pairs(s_B + (k0 + k) * NP + j * R, B);
-                    if (kMode != kRangeState) lds_pairs(s_C + (k0 + k) * NP + j * R, C);
+                    f32x2 B[P], C[P];
+                    lds_pairs(&s_B[b][(k0 + k) * NP + j * R], B);
+                    if (kOut) lds_pairs(&s_C[b][(k0 + k) * NP + j * R], C);
 #pragma unroll
-                    for (int p = 0; p < P; ++p) {
-                        h[p] = fma2(ex2_pair(mul2(vv, A[p])), h[p], mul2(uu, B[p]));
-                        if (kMode != kRangeState) acc = fma2(h[p], C[p], acc);
+                    for (int q = 0; q < Q; ++q) {
+                        const float2 vu = s_vu[b][(k0 + k) * CT + ch + q * CS];
+                        const f32x2 vv = pack2(vu.x, vu.x), uu = pack2(vu.y, vu.y);
+                        f32x2 acc;
+#pragma unroll
+                        for (int p = 0; p < P; ++p) {
+                            h[q][p] = fma2(ex2_pair(mul2(vv, A[q][p])), h[q][p], mul2(uu, B[p]));
+                            if (kOut) acc = p ? fma2(h[q][p], C[p], acc) : mul2(h[q][p], C[p]);
+                        }
+                        if (kOut) {
+                            yv[q][k] = sum2(acc);
+                            if (L <= 4) s_y[b][((k0 + k) * CT + ch + q * CS) * YP + j] = yv[q][k];
+                        } else {
+                            vsum[q] += vu.x;
+                        }
                     }
-                    yv[k] = sum2(acc);
-                    if (kMode == kRangeState) vsum += v;
                 }
-                if (kMode != kRangeState) {
-                    const int first = reduce_lanes<TG, L, 1>(yv, lane);
-                    constexpr int kLeft = reduce_left(TG, L);
-                    constexpr int kSame = L > TG ? L / TG : 1;   // lanes that end with the same sum
-                    if (j % kSame == 0) {
+                if (kOut && L > 4) {
+                    // four partial sums are left to the output step: lanes that differ in the upper bits are added
+                    constexpr int kUp = L > 4 ? L / 4 : 1, kLeft = reduce_left(TG, kUp), kSame = kUp > TG ? kUp / TG : 1;
 #pragma unroll
-                        for (int i = 0; i < kLeft; ++i) s_y[(k0 + first + i) * CT + ch] = yv[i];
+                    for (int q = 0; q < Q; ++q) {
+                        const int first = reduce_lanes<TG, kUp, 4>(yv[q], lane);
+                        if ((j / 4) % kSame == 0) {
+#pragma unroll
+                            for (int i = 0; i < kLeft; ++i)
+                                s_y[b][((k0 + first + i) * CT + ch + q * CS) * YP + j % 4] = yv[q][i];
+                        }
                     }
                 }
             }
-            __syncthreads();
-            if (kMode != kRangeState) {
-#pragma unroll
-                for (int i = 0; i < E; ++i) {
-                    const int k = st + i * RS;
-                    if (slive && k < KT && t + k < t1) {
-                        float y = fmaf(skip, xc[i], s_y[k * CT + sc]);
-                        if (a.z) y *= silu_approx(raw_value<TIn>(zc[i]));
-                        st_act(a.y, (t + k) * a.dim + ds, y, a.y_bf16);
-                    }
-                }
-            }
-            t = t1;
-            t1 = t2;
+            t += n;
+            rel += n;
+            left -= n;
+            before = n;
+            n = n2;
+            b ^= 1;
         }
+        __syncthreads();
+        if (kOut) output(t - before, before, b ^ 1);
+        __syncthreads();                           // the next sequence stages into either buffer
     };
 
     // Row of the sequence's state, -1 for a bad slot; whether it is read.
@@ -250,10 +344,19 @@ selective_scan_kernel(SelScanArgs a)
         report_status(a.status_dev, kStatusDeviceInput);
         return -1;
     };
-    auto load_initial = [&](long row, bool init) {
+    // Every channel's states from rows[row] (or zero).
+    auto load_all = [&](const float *rows, long row, f32x2 (&to)[Q][P]) {
 #pragma unroll
-        for (int p = 0; p < P; ++p) h[p] = pack2(0.f, 0.f);
-        if (init && live) load_states<R>(a.initial + (row * a.dim + d) * N, j, N, h);
+        for (int q = 0; q < Q; ++q) {
+#pragma unroll
+            for (int p = 0; p < P; ++p) to[q][p] = pack2(0.f, 0.f);
+            if (rows && live(q)) load_states<R>(row_of(rows, row, q), j, N, to[q]);
+        }
+    };
+    auto store_all = [&](float *rows, long row) {
+#pragma unroll
+        for (int q = 0; q < Q; ++q)
+            if (live(q)) store_states<R>(const_cast<float *>(row_of(rows, row, q)), j, N, h[q]);
     };
     auto one_sequence = [&](int s, long r0, long r1) {   // its tokens within [r0, r1)
         long lo, hi;
@@ -268,27 +371,27 @@ selective_scan_kernel(SelScanArgs a)
         if (kMode == kRangeOut && lo < r0) {
             // the state entering this range: the ranges since the sequence's start, folded
             const int first = (int)(lo / a.span), own = (int)(r0 / a.span);
+            load_all(a.range_state, first, h);
+            for (int i = first + 1; i < own; ++i) {
+                f32x2 e[Q][P];
+                load_all(a.range_state, i, e);
 #pragma unroll
-            for (int p = 0; p < P; ++p) h[p] = pack2(0.f, 0.f);
-            for (int q = first; q < own && live; ++q) {
-                f32x2 e[P];
-                load_states<R>(a.range_state + ((long)q * a.dim + d) * N, j, N, e);
-                const float v = a.range_dt[(long)q * a.dim + d];
+                for (int q = 0; q < Q; ++q) {
+                    const float v = live(q) ? a.range_dt[(long)i * a.dim + d0 + q * CS] : 0.f;
 #pragma unroll
-                for (int p = 0; p < P; ++p) h[p] = q == first ? e[p] : fma2(ex2_pair(mul2(pack2(v, v), A[p])), h[p], e[p]);
+                    for (int p = 0; p < P; ++p)
+                        h[q][p] = fma2(ex2_pair(mul2(pack2(v, v), A[q][p])), h[q][p], e[q][p]);
+                }
             }
         } else if (kMode == kRangeOut && hi > r1) {
             // its row may be written (in place) by the range it ends in: the copy is read
-#pragma unroll
-            for (int p = 0; p < P; ++p) h[p] = pack2(0.f, 0.f);
-            if (live) load_states<R>(a.range_initial + ((r0 / a.span) * a.dim + d) * N, j, N, h);
+            load_all(a.range_initial, r0 / a.span, h);
         } else {
-            load_initial(row, init);
+            load_all(init ? a.initial : nullptr, row, h);
         }
         const long b = max(lo, r0), e = min(hi, r1);
         if (b < e) run(b, e, lo, lo / kSavedEvery + s);
-        if (hi <= r1 && a.final && live && (lo < hi || a.final != a.initial || !init))
-            store_states<R>(a.final + (row * a.dim + d) * N, j, N, h);
+        if (hi <= r1 && a.final && (lo < hi || a.final != a.initial || !init)) store_all(a.final, row);
     };
 
     if (kMode == kWhole) {
@@ -301,12 +404,13 @@ selective_scan_kernel(SelScanArgs a)
         if (!seq_range(a, T, s, lo, hi) || lo >= r1 || hi <= r1) return;
         const long row = state_row(s, init);
         if (row < 0) return;
-        load_initial(row, init && lo >= r0);
-        if (lo >= r0 && live) store_states<R>(a.range_initial + ((long)unit * a.dim + d) * N, j, N, h);
+        load_all(init && lo >= r0 ? a.initial : nullptr, row, h);
+        if (lo >= r0) store_all(a.range_initial, unit);
         run(max(lo, r0), r1, lo, 0);
-        if (!live) return;
-        store_states<R>(a.range_state + ((long)unit * a.dim + d) * N, j, N, h);
-        if (j == 0) a.range_dt[(long)unit * a.dim + d] = vsum;
+        store_all(a.range_state, unit);
+#pragma unroll
+        for (int q = 0; q < Q; ++q)
+            if (j == 0 && live(q)) a.range_dt[(long)unit * a.dim + d0 + q * CS] = vsum[q];
     } else {
         const long r0 = (long)unit * a.span, r1 = min(r0 + a.span, T);
         int s = seq_of(a, r0);
@@ -320,19 +424,19 @@ selective_scan_kernel(SelScanArgs a)
     }
 }
 
-template <typename TIn, typename TDt, int R, int L>
+template <typename TIn, typename TDt, int R, int L, int Q>
 cudaError_t launch_shape(const SelScanArgs &a, cudaStream_t stream)
 {
-    const int gdim = a.dim / a.ngroups, CT = ScanShape<R, L>::CT;
+    const int gdim = a.dim / a.ngroups, CT = ScanShape<R, L, Q>::CT;
     const long long tiles = (long long)((gdim + CT - 1) / CT) * a.ngroups;
     if (tiles * (a.ranges ? a.ranges : a.nseq) > 0x7fffffffLL) return cudaErrorInvalidValue;
     if (!a.ranges) {
-        selective_scan_kernel<TIn, TDt, R, L, kWhole><<<(unsigned)(tiles * a.nseq), kThreads, 0, stream>>>(a);
+        selective_scan_kernel<TIn, TDt, R, L, Q, kWhole><<<(unsigned)(tiles * a.nseq), kThreads, 0, stream>>>(a);
         return cudaGetLastError();
     }
     if (a.ranges > 1)
-        selective_scan_kernel<TIn, TDt, R, L, kRangeState><<<(unsigned)(tiles * (a.ranges - 1)), kThreads, 0, stream>>>(a);
-    selective_scan_kernel<TIn, TDt, R, L, kRangeOut><<<(unsigned)(tiles * a.ranges), kThreads, 0, stream>>>(a);
+        selective_scan_kernel<TIn, TDt, R, L, Q, kRangeState><<<(unsigned)(tiles * (a.ranges - 1)), kThreads, 0, stream>>>(a);
+    selective_scan_kernel<TIn, TDt, R, L, Q, kRangeOut><<<(unsigned)(tiles * a.ranges), kThreads, 0, stream>>>(a);
     return cudaGetLastError();
 }
 
@@ -340,21 +444,43 @@ template <typename TIn, typename TDt>
 cudaError_t launch_types(const SelScanArgs &a, cudaStream_t stream)
 {
     const int N = a.d_state;
-    if (N <= 4) return launch_shape<TIn, TDt, 4, 1>(a, stream);
-    if (N <= 8) return launch_shape<TIn, TDt, 4, 2>(a, stream);
-    if (N <= 16) return launch_shape<TIn, TDt, 4, 4>(a, stream);
-    if (N <= 32) return launch_shape<TIn, TDt, 4, 8>(a, stream);
-    if (N <= 64) return launch_shape<TIn, TDt, 4, 16>(a, stream);
-    if (N <= 128) return launch_shape<TIn, TDt, 4, 32>(a, stream);
-    return launch_shape<TIn, TDt, 8, 32>(a, stream);
+    if (N <= 4) return launch_shape<TIn, TDt, 4, 1, 1>(a, stream);
+    if (N <= 8) return launch_shape<TIn, TDt, 4, 2, 1>(a, stream);
+    if (N <= 16) return launch_shape<TIn, TDt, 4, 4, 1>(a, stream);
+    if (N <= 32) return launch_shape<TIn, TDt, 4, 8, 1>(a, stream);
+    if (N <= 64) return launch_shape<TIn, TDt, 4, 16, 1>(a, stream);
+    if (N <= 128) return launch_shape<TIn, TDt, 4, 32, 1>(a, stream);
+    return launch_shape<TIn, TDt, 8, 32, 1>(a, stream);
 }
 
 }  // namespace
 
+// Lanes of a warp that share a channel.
+static int lanes_for(int N) { return N <= 4 ? 1 : N <= 8 ? 2 : N <= 16 ? 4 : N <= 32 ? 8 : N <= 64 ? 16 : 32; }
+
+// A sequence is a chain of its tokens: nseq * dim channels give
+// nseq * dim * lanes / 32 warps, however long it is.  Cutting the stream costs
+// the ranges' first pass (about 0.6 of the work again), so it is done where
+// the chains fill less than a third of the warps that the device holds, into
+// as many ranges as fill it, of at least 128 tokens.
 int selective_scan_ranges(int nseq, long T, int dim, int d_state, int ngroups, int *span)
 {
     *span = 0;
-    return 0;
+    int dev = 0, sms = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms <= 0) {
+        cudaGetLastError();
+        return 0;
+    }
+    const double warps = (double)dim * lanes_for(d_state) / 32, room = 28.0 * sms;
+    if (warps * nseq * 3 > room) return 0;
+    long ranges = (long)(room / warps);
+    if (ranges > T / 128) ranges = T / 128;
+    if (ranges > 256) ranges = 256;
+    if (ranges < 3 || ranges <= 2L * nseq) return 0;
+    const long n = (T + ranges - 1) / ranges, len = (n + kSavedEvery - 1) / kSavedEvery * kSavedEvery;
+    *span = (int)len;
+    return (int)((T + len - 1) / len);
 }
 
 cudaError_t launch_selective_scan(const SelScanArgs &a, cudaStream_t stream)

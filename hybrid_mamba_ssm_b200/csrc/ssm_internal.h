@@ -146,6 +146,7 @@ struct SelScanArgs {
     const int32_t *cu_seqlens;
     int dim, d_state, ngroups;
     int in_bf16, dt_bf16, y_bf16;
+    int pairs;                    // x, dt, z: two adjacent channels (an even and the next) are one aligned access
     const void *x, *dt, *B, *C, *z;   // z nullptr: no gate
     long x_stride, dt_stride, B_stride, C_stride, z_stride;
     const float *A;               // [dim][d_state]

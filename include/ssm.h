@@ -500,7 +500,7 @@ SSM_API int ssm_gated_rmsnorm(int rows, int dim, int group_size, int y_dtype, co
  *
  * Layouts: x, dt, z [T][dim], B, C [T][ngroups][d_state], each with its own
  * distance between tokens (`*_stride`, in elements, at least the row's
- * length), so that the halves of an input projection or the slices of a
+ * length and at most 2^24), so that the halves of an input projection or the slices of a
  * low-rank projection are passed as they are.  These five (and dy below) need
  * only the alignment of their element; every other pointer is 16-byte
  * aligned.  x, B, C, z have in_dtype, dt has dt_dtype: in_dtype or SSM_F32.
