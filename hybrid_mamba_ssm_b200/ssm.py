@@ -9,7 +9,6 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
-import math
 import os
 from typing import NamedTuple
 
@@ -614,46 +613,55 @@ def _enter(device, stream):
 
 
 _NO_SCOPE = contextlib.nullcontext()
+_F32, _I32 = torch.float32, torch.int32
 
 
 def _scope(t, stream):
     """The device of t and the given stream made current, so that what a call
     allocates belongs to the stream that uses it."""
-    if not t.is_cuda:
+    dev = t.get_device()
+    if dev < 0:
         raise ValueError("tensors must be CUDA tensors")
-    if stream is None and t.device.index == torch.cuda.current_device():
+    if stream is None and dev == torch.cuda.current_device():
         return _NO_SCOPE
     return _enter(t.device, stream)
 
 
-def _dev_like(t, name, like, dtype=None, shape=None):
-    """_dev, and t on like's device, of the given shape."""
+def _raw_stream(dev) -> int:
+    return torch.cuda.current_stream(dev).cuda_stream
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _dev_like(t, name, dev, dtype=None, shape=None):
+    """None, or t's address: a contiguous tensor on device dev, of the given type and shape."""
     if t is None:
-        return
+        return None
+    if t.get_device() == dev and t.is_contiguous() and (dtype is None or t.dtype is dtype) \
+            and (shape is None or t.shape == shape):
+        return t.data_ptr()
     _dev(t, name, dtype)
-    if t.device != like.device:
-        raise ValueError(f"{name} is on {t.device}, not {like.device}")
-    if shape is not None and tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, not on device {dev}")
+    raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
-def _token_rows(t, name, lead, width, like, dtype):
-    """Elements between the tokens of an activation whose leading axes are
-    ``lead`` ([T], or [nseq, L]) and whose trailing axes make a row of
-    ``width`` adjacent elements."""
-    if not t.is_cuda or t.device != like.device:
-        raise ValueError(f"{name} must be a CUDA tensor on {like.device}")
-    if t.dtype != dtype:
+def _token_rows(t, name, lead, row, dev, dtype):
+    """Elements between the tokens of an activation of shape lead + row (lead:
+    (T,), or (nseq, L)), whose rows are contiguous and equally spaced."""
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be a CUDA tensor on device {dev}")
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     shape, strides = t.shape, t.stride()
+    if shape != lead + row:
+        raise ValueError(f"{name} must have shape {lead + row}, got {tuple(shape)}")
     k = len(lead)
-    if tuple(shape[:k]) != tuple(lead) or math.prod(shape[k:]) != width:
-        raise ValueError(f"{name} must have shape {tuple(lead)} + rows of {width}, got {tuple(shape)}")
-    step = 1
-    for size, stride in zip(reversed(shape[k:]), reversed(strides[k:])):
-        if size > 1 and stride != step:
-            raise ValueError(f"the rows of {name} must be contiguous")
-        step *= size
+    width = row[0] if len(row) == 1 else row[0] * row[1]
+    if (row[-1] > 1 and strides[-1] != 1) or (len(row) == 2 and row[0] > 1 and strides[k] != row[1]):
+        raise ValueError(f"the rows of {name} must be contiguous")
     if k == 1:
         return strides[0] if shape[0] > 1 else width
     n, length = lead
@@ -663,10 +671,10 @@ def _token_rows(t, name, lead, width, like, dtype):
     return token
 
 
-def _scan_lead(x, cu_seqlens):
+def _scan_lead(x, cu_seqlens, dev):
     """(leading axes, nseq, seqlen, tokens, dim) of an x [nseq, L, dim] or packed [T, dim]."""
     if cu_seqlens is not None:
-        _dev_like(cu_seqlens, "cu_seqlens", x, torch.int32)
+        _dev_like(cu_seqlens, "cu_seqlens", dev, _I32)
         if x.dim() != 2 or cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 1:
             raise ValueError("packed x must be [T, dim] with cu_seqlens [nseq+1]")
         T, dim = x.shape
@@ -677,38 +685,43 @@ def _scan_lead(x, cu_seqlens):
     return (n, length), n, length, n * length, dim
 
 
-def _scan_operands(lead, dim, x, dt, A, B, C, D, z, dt_bias):
-    """Checks the operands of a per-channel scan; their token strides."""
-    in_code, dt_code = _dtype_code(x.dtype), _dtype_code(dt.dtype)
+def _scan_operands(lead, dim, dev, x, dt, A, B, C, D, z, dt_bias, dt_softplus, dt_limit):
+    """Checks the operands of a per-channel scan.  (d_state, groups, and the
+    arguments in_dtype .. dt_params of the call, around dy where it takes one)."""
+    dtype = x.dtype
+    in_code, dt_code = _dtype_code(dtype), _dtype_code(dt.dtype)
     if A.dim() != 2 or B.dim() != len(lead) + 2:
         raise ValueError("A must be [dim, d_state], B and C the tokens' [ngroups, d_state]")
     N, G = A.shape[1], B.shape[-2]
-    _dev_like(A, "A", x, torch.float32, (dim, N))
-    _dev_like(D, "D", x, torch.float32, (dim,))
-    _dev_like(dt_bias, "dt_bias", x, torch.float32, (dim,))
-    if tuple(B.shape[-2:]) != (G, N) or tuple(C.shape[-2:]) != (G, N):
-        raise ValueError(f"B and C must be [..., {G}, {N}]")
-    xs = _token_rows(x, "x", lead, dim, x, x.dtype)
-    dts = _token_rows(dt, "dt", lead, dim, x, dt.dtype)
-    Bs = _token_rows(B, "B", lead, G * N, x, x.dtype)
-    Cs = _token_rows(C, "C", lead, G * N, x, x.dtype)
-    zs = 0 if z is None else _token_rows(z, "z", lead, dim, x, x.dtype)
-    return in_code, dt_code, N, G, xs, dts, Bs, Cs, zs
+    row, bc = (dim,), (G, N)
+    a = _dev_like(A, "A", dev, _F32, (dim, N))
+    d = _dev_like(D, "D", dev, _F32, row)
+    params = None
+    if dt_bias is not None or dt_softplus or dt_limit is not None:
+        bias = _dev_like(dt_bias, "dt_bias", dev, _F32, row)
+        lo, hi = (0.0, 0.0) if dt_limit is None else dt_limit
+        params = ctypes.byref(DtParams(bias, bool(dt_softplus), dt_limit is not None, lo, hi))
+    xs = _token_rows(x, "x", lead, row, dev, dtype)
+    dts = _token_rows(dt, "dt", lead, row, dev, dt.dtype)
+    Bs = _token_rows(B, "B", lead, bc, dev, dtype)
+    Cs = _token_rows(C, "C", lead, bc, dev, dtype)
+    zs = 0 if z is None else _token_rows(z, "z", lead, row, dev, dtype)
+    return N, G, in_code, (x.data_ptr(), xs, dt_code, dt.data_ptr(), dts, a, B.data_ptr(), Bs, C.data_ptr(), Cs,
+                           d, _addr(z), zs, params)
 
 
-def _bytes(t) -> int:
-    return 0 if t is None else t.numel() * t.element_size()
-
-
-def _workspace(workspace, size, like):
-    """"auto": a workspace of `size()` bytes (None where that is 0); else what was given."""
+def _workspace(workspace, size, like, dev):
+    """(tensor to keep, address, bytes) of a workspace: "auto" allocates `size` bytes."""
     if isinstance(workspace, str):
         if workspace != "auto":
             raise ValueError('workspace must be a CUDA tensor, None or "auto"')
-        n = size()
-        return torch.empty(n, dtype=torch.uint8, device=like.device) if n else None
-    _dev_like(workspace, "workspace", like)
-    return workspace
+        if not size:
+            return None, None, 0
+        workspace = like.new_empty(size, dtype=torch.uint8)
+        return workspace, workspace.data_ptr(), size
+    if workspace is None:
+        return None, None, 0
+    return workspace, _dev_like(workspace, "workspace", dev), workspace.numel() * workspace.element_size()
 
 
 def selective_scan_fwd(x, dt, A, B, C, D=None, z=None, initial_state=None, cu_seqlens=None,
@@ -733,36 +746,34 @@ def selective_scan_fwd(x, dt, A, B, C, D=None, z=None, initial_state=None, cu_se
     Returns (y, final_state), or (y, final_state, saved) with save_states.
     """
     with _scope(x, stream):
-        lead, nseq, seqlen, T, dim = _scan_lead(x, cu_seqlens)
-        in_code, dt_code, N, G, xs, dts, Bs, Cs, zs = _scan_operands(lead, dim, x, dt, A, B, C, D, z, dt_bias)
-        pool = nseq
+        dev = x.get_device()
+        lead, nseq, seqlen, T, dim = _scan_lead(x, cu_seqlens, dev)
+        N, G, in_code, operands = _scan_operands(lead, dim, dev, x, dt, A, B, C, D, z, dt_bias, dt_softplus, dt_limit)
+        rows = nseq
         if slot_idx is not None:
-            _dev_like(slot_idx, "slot_idx", x, torch.int32, (nseq,))
             states = final_state if final_state is not None else initial_state
             if states is None:
                 raise ValueError("slot_idx needs a state pool")
-            pool = states.shape[0]
-        _dev_like(has_initial_state, "has_initial_state", x, torch.int32, (nseq,))
-        _dev_like(initial_state, "initial_state", x, torch.float32, (pool, dim, N))
-        if final_state is None and return_final_state and slot_idx is None:
-            final_state = torch.empty((nseq, dim, N), dtype=torch.float32, device=x.device)
-        _dev_like(final_state, "final_state", x, torch.float32, (pool, dim, N))
-        _dev_like(status, "status", x, torch.int32)
+            rows = states.shape[0]
+        elif final_state is None and return_final_state:
+            final_state = x.new_empty((nseq, dim, N), dtype=_F32)
         if y is None:
-            y = torch.empty(x.shape, dtype=y_dtype or x.dtype, device=x.device)
-        _dev_like(y, "y", x, y_dtype, x.shape)
-        saved = None
+            y = x.new_empty(x.shape, dtype=y_dtype or x.dtype)
+        saved = ws = ws_ptr = None
+        ws_bytes = 0
         if save_states:
-            saved = torch.empty(selective_scan_saved_size(nseq, T, dim, N) // 4, dtype=torch.float32,
-                                device=x.device)
-        workspace = None if save_states else _workspace(
-            workspace, lambda: lib.selective_scan_workspace_size(nseq, T, dim, N, G), x)
-        st = lib.selective_scan_fwd(nseq, seqlen, _ptr(cu_seqlens), dim, N, G, in_code, _ptr(x), xs,
-                                    dt_code, _ptr(dt), dts, _ptr(A), _ptr(B), Bs, _ptr(C), Cs, _ptr(D),
-                                    _ptr(z), zs, _dt_params(dt_bias, dt_softplus, dt_limit),
-                                    _ptr(initial_state), _ptr(final_state), pool, _ptr(slot_idx),
-                                    _ptr(has_initial_state), _dtype_code(y.dtype), _ptr(y), _ptr(saved),
-                                    _ptr(workspace), _bytes(workspace), _ptr(status), _stream(None))
+            saved = x.new_empty(lib.selective_scan_saved_size(nseq, T, dim, N) // 4, dtype=_F32)
+        else:
+            size = lib.selective_scan_workspace_size(nseq, T, dim, N, G) if workspace == "auto" else 0
+            ws, ws_ptr, ws_bytes = _workspace(workspace, size, x, dev)
+        st = lib.selective_scan_fwd(
+            nseq, seqlen, _addr(cu_seqlens), dim, N, G, in_code, *operands,
+            _dev_like(initial_state, "initial_state", dev, _F32, (rows, dim, N)),
+            _dev_like(final_state, "final_state", dev, _F32, (rows, dim, N)), rows,
+            _dev_like(slot_idx, "slot_idx", dev, _I32, (nseq,)),
+            _dev_like(has_initial_state, "has_initial_state", dev, _I32, (nseq,)),
+            _dtype_code(y.dtype), _dev_like(y, "y", dev, y_dtype, x.shape), _addr(saved), ws_ptr, ws_bytes,
+            _dev_like(status, "status", dev, _I32), _raw_stream(dev))
     _check(st, "selective_scan_fwd")
     return (y, final_state, saved) if save_states else (y, final_state)
 
@@ -799,34 +810,28 @@ def selective_scan_bwd(dy, x, dt, A, B, C, saved, D=None, z=None, dfinal_state=N
     dfinal_state : [nseq, dim, d_state] fp32 or None.  The gradients have their
     inputs' shapes and types (contiguous)."""
     with _scope(x, stream):
-        lead, nseq, seqlen, T, dim = _scan_lead(x, cu_seqlens)
-        in_code, dt_code, N, G, xs, dts, Bs, Cs, zs = _scan_operands(lead, dim, x, dt, A, B, C, D, z, dt_bias)
-        dys = _token_rows(dy, "dy", lead, dim, x, x.dtype)
-        _dev_like(saved, "saved", x, torch.float32)
-        if _bytes(saved) != selective_scan_saved_size(nseq, T, dim, N):
+        dev = x.get_device()
+        lead, nseq, seqlen, T, dim = _scan_lead(x, cu_seqlens, dev)
+        N, G, in_code, operands = _scan_operands(lead, dim, dev, x, dt, A, B, C, D, z, dt_bias, dt_softplus, dt_limit)
+        dys = _token_rows(dy, "dy", lead, (dim,), dev, x.dtype)
+        if saved.numel() * 4 != lib.selective_scan_saved_size(nseq, T, dim, N):
             raise ValueError("saved is not that of a forward call of these sizes")
-        _dev_like(dfinal_state, "dfinal_state", x, torch.float32, (nseq, dim, N))
-        _dev_like(status, "status", x, torch.int32)
 
         # a batch of no sequences launches nothing: its sums are zero
-        empty = torch.zeros if nseq == 0 else torch.empty
-
-        def new(shape, dtype=torch.float32):
-            return empty(shape, dtype=dtype, device=x.device)
-
+        new = x.new_zeros if nseq == 0 else x.new_empty
         g = SelectiveScanGrads(
-            new(x.shape, x.dtype), new(dt.shape, dt.dtype), new((dim, N)), new(B.shape, x.dtype),
-            new(C.shape, x.dtype), None if D is None else new((dim,)),
-            None if z is None else new(z.shape, x.dtype), None if dt_bias is None else new((dim,)),
-            new((nseq, dim, N)) if want_dinitial else None)
-        workspace = _workspace(workspace, lambda: lib.selective_scan_bwd_workspace_size(nseq, T, dim, N, G), x)
-        st = lib.selective_scan_bwd(nseq, seqlen, _ptr(cu_seqlens), dim, N, G, in_code, _ptr(dy), dys,
-                                    _ptr(x), xs, dt_code, _ptr(dt), dts, _ptr(A), _ptr(B), Bs, _ptr(C), Cs,
-                                    _ptr(D), _ptr(z), zs, _dt_params(dt_bias, dt_softplus, dt_limit),
-                                    _ptr(saved), _ptr(dfinal_state), _ptr(g.dx), _ptr(g.ddt), _ptr(g.dA),
-                                    _ptr(g.dB), _ptr(g.dC), _ptr(g.dD), _ptr(g.dz), _ptr(g.ddt_bias),
-                                    _ptr(g.dinitial_state), _ptr(workspace), _bytes(workspace),
-                                    _ptr(status), _stream(None))
+            new(x.shape), new(dt.shape, dtype=dt.dtype), new((dim, N), dtype=_F32), new(B.shape), new(C.shape),
+            None if D is None else new((dim,), dtype=_F32), None if z is None else new(z.shape),
+            None if dt_bias is None else new((dim,), dtype=_F32),
+            new((nseq, dim, N), dtype=_F32) if want_dinitial else None)
+        size = lib.selective_scan_bwd_workspace_size(nseq, T, dim, N, G) if workspace == "auto" else 0
+        ws, ws_ptr, ws_bytes = _workspace(workspace, size, x, dev)
+        st = lib.selective_scan_bwd(
+            nseq, seqlen, _addr(cu_seqlens), dim, N, G, in_code, dy.data_ptr(), dys, *operands,
+            _dev_like(saved, "saved", dev, _F32),
+            _dev_like(dfinal_state, "dfinal_state", dev, _F32, (nseq, dim, N)),
+            *[_addr(t) for t in (g.dx, g.ddt, g.dA, g.dB, g.dC, g.dD, g.dz, g.ddt_bias, g.dinitial_state)],
+            ws_ptr, ws_bytes, _dev_like(status, "status", dev, _I32), _raw_stream(dev))
     _check(st, "selective_scan_bwd")
     return g
 
@@ -849,19 +854,17 @@ def selective_state_update(state, x, dt, A, B, C, D=None, z=None, slot_idx=None,
     with _scope(x, stream):
         if x.dim() != 2:
             raise ValueError("x must be [batch, dim]")
+        dev = x.get_device()
         batch, dim = x.shape
-        in_code, dt_code, N, G, xs, dts, Bs, Cs, zs = _scan_operands((batch,), dim, x, dt, A, B, C, D, z, dt_bias)
-        _dev_like(slot_idx, "slot_idx", x, torch.int32, (batch,))
+        N, G, in_code, operands = _scan_operands((batch,), dim, dev, x, dt, A, B, C, D, z, dt_bias, dt_softplus,
+                                                 dt_limit)
         rows = batch if slot_idx is None else state.shape[0]
-        _dev_like(state, "state", x, torch.float32, (rows, dim, N))
-        _dev_like(status, "status", x, torch.int32)
         if y is None:
-            y = torch.zeros((batch, dim), dtype=y_dtype or x.dtype, device=x.device)
-        _dev_like(y, "y", x, y_dtype, (batch, dim))
-        st = lib.selective_state_update(batch, dim, N, G, _ptr(state), rows, _ptr(slot_idx), in_code,
-                                        _ptr(x), xs, dt_code, _ptr(dt), dts, _ptr(A), _ptr(B), Bs, _ptr(C),
-                                        Cs, _ptr(D), _ptr(z), zs, _dt_params(dt_bias, dt_softplus, dt_limit),
-                                        _dtype_code(y.dtype), _ptr(y), _ptr(status), _stream(None))
+            y = x.new_zeros((batch, dim), dtype=y_dtype or x.dtype)
+        st = lib.selective_state_update(
+            batch, dim, N, G, _dev_like(state, "state", dev, _F32, (rows, dim, N)), rows,
+            _dev_like(slot_idx, "slot_idx", dev, _I32, (batch,)), in_code, *operands, _dtype_code(y.dtype),
+            _dev_like(y, "y", dev, y_dtype, (batch, dim)), _dev_like(status, "status", dev, _I32), _raw_stream(dev))
     _check(st, "selective_state_update")
     return y
 
@@ -875,53 +878,55 @@ def causal_conv1d_bwd(dy, x, weight, bias=None, initial_state=None, dfinal_state
     None.  Returns (dx, dweight, dbias, dinitial_state); dbias is None without
     bias, dinitial_state None without initial_state."""
     with _scope(x, stream):
-        _dev(x, "x")
+        dev = x.get_device()
         in_code = _dtype_code(x.dtype)
-        _, nseq, seqlen, T, dim = _scan_lead(x, cu_seqlens)
+        _, nseq, seqlen, T, dim = _scan_lead(x, cu_seqlens, dev)
         if weight.dim() != 2:
             raise ValueError("weight must be [dim, width]")
         width = weight.shape[1]
-        _dev_like(dy, "dy", x, x.dtype, x.shape)
-        _dev_like(weight, "weight", x, torch.float32, (dim, width))
-        _dev_like(bias, "bias", x, torch.float32, (dim,))
-        _dev_like(initial_state, "initial_state", x, x.dtype, (nseq, dim, width - 1))
-        _dev_like(dfinal_state, "dfinal_state", x, x.dtype, (nseq, dim, width - 1))
-        _dev_like(status, "status", x, torch.int32)
-        dx, dweight = torch.empty_like(x), torch.empty_like(weight)
-        dbias = None if bias is None else torch.empty_like(bias)
-        dinitial = None if initial_state is None else torch.empty_like(initial_state)
-        workspace = _workspace(workspace, lambda: lib.causal_conv1d_bwd_workspace_size(T, dim, width), x)
-        st = lib.causal_conv1d_bwd(nseq, seqlen, _ptr(cu_seqlens), dim, width, in_code, _ptr(dy), _ptr(x),
-                                   _ptr(weight), _ptr(bias), _activation(activation), _ptr(initial_state),
-                                   _ptr(dfinal_state), _ptr(dx), _ptr(dweight), _ptr(dbias), _ptr(dinitial),
-                                   _ptr(workspace), _bytes(workspace), _ptr(status), _stream(None))
+        dx, dweight = x.new_empty(x.shape), weight.new_empty((dim, width))
+        dbias = None if bias is None else weight.new_empty((dim,))
+        line = (nseq, dim, width - 1)
+        dinitial = None if initial_state is None else x.new_empty(line)
+        size = lib.causal_conv1d_bwd_workspace_size(T, dim, width) if workspace == "auto" else 0
+        ws, ws_ptr, ws_bytes = _workspace(workspace, size, x, dev)
+        st = lib.causal_conv1d_bwd(
+            nseq, seqlen, _addr(cu_seqlens), dim, width, in_code,
+            _dev_like(dy, "dy", dev, x.dtype, x.shape), _dev_like(x, "x", dev),
+            _dev_like(weight, "weight", dev, _F32, (dim, width)), _dev_like(bias, "bias", dev, _F32, (dim,)),
+            _activation(activation), _dev_like(initial_state, "initial_state", dev, x.dtype, line),
+            _dev_like(dfinal_state, "dfinal_state", dev, x.dtype, line), dx.data_ptr(), dweight.data_ptr(),
+            _addr(dbias), _addr(dinitial), ws_ptr, ws_bytes, _dev_like(status, "status", dev, _I32), _raw_stream(dev))
     _check(st, "causal_conv1d_bwd")
     return dx, dweight, dbias, dinitial
-
-
-class Pool(ctypes.Structure):
-    """ssm_pool: row i is row_bytes bytes at base + i * row_stride."""
-    _fields_ = [("base", ctypes.c_void_p), ("row_bytes", ctypes.c_int64), ("row_stride", ctypes.c_int64)]
 
 
 def _pools(pools):
     """(ssm_pool array, count, max_slots, a tensor of them) of tensors [max_slots, ...]
     whose rows are contiguous."""
-    pools = [pools] if isinstance(pools, torch.Tensor) else list(pools)
+    pools = (pools,) if isinstance(pools, torch.Tensor) else pools
     if not pools:
         raise ValueError("no pools given")
-    first, arr = pools[0], (Pool * len(pools))()
-    for k, p in enumerate(pools):
-        if not p.is_cuda or p.device != first.device:
+    first = pools[0]
+    dev, slots = first.get_device(), first.shape[0] if first.dim() else -1
+    fields, shape, strides, size = [], None, None, 0
+    for p in pools:
+        # the pools of a stack's layers are mostly alike: a layout is looked at once
+        if p.shape != shape or p.stride() != strides or p.element_size() != size:
+            shape, strides, size = p.shape, p.stride(), p.element_size()
+            if p.dim() < 1 or shape[0] != slots:
+                raise ValueError("pools must be tensors [max_slots, ...] with the same number of slots")
+            step = 1
+            for n, stride in zip(reversed(shape[1:]), reversed(strides[1:])):
+                if n > 1 and stride != step:
+                    raise ValueError("the rows of a pool must be contiguous")
+                step *= n
+            row, pitch = step * size, (strides[0] if slots > 1 else step) * size
+        if p.get_device() != dev:
             raise ValueError("pools must be CUDA tensors on one device")
-        if p.dim() < 1 or p.shape[0] != first.shape[0]:
-            raise ValueError("pools must have the same number of slots")
-        row = p.select(0, 0) if p.shape[0] else p
-        if not row.is_contiguous():
-            raise ValueError("the rows of a pool must be contiguous")
-        nbytes = row.numel() * p.element_size()
-        arr[k] = Pool(p.data_ptr(), nbytes, p.stride(0) * p.element_size() if p.shape[0] > 1 else nbytes)
-    return arr, len(pools), first.shape[0], first
+        fields += p.data_ptr(), row, pitch
+    # ssm_pool is three 64-bit fields: base, row_bytes, row_stride
+    return (ctypes.c_int64 * len(fields))(*fields), len(pools), slots, first
 
 
 def ssm_pool_copy(pools, src_idx, dst_idx, status=None, stream=None) -> None:
@@ -931,11 +936,10 @@ def ssm_pool_copy(pools, src_idx, dst_idx, status=None, stream=None) -> None:
     entry with a negative index is skipped."""
     arr, n, slots, like = _pools(pools)
     with _scope(like, stream):
-        _dev_like(src_idx, "src_idx", like, torch.int32)
-        _dev_like(dst_idx, "dst_idx", like, torch.int32, src_idx.shape)
-        _dev_like(status, "status", like, torch.int32)
-        st = lib.ssm_pool_copy(n, arr, slots, src_idx.numel(), _ptr(src_idx), _ptr(dst_idx), _ptr(status),
-                               _stream(None))
+        dev, pairs = like.get_device(), src_idx.shape[0]
+        st = lib.ssm_pool_copy(n, arr, slots, pairs, _dev_like(src_idx, "src_idx", dev, _I32, (pairs,)),
+                               _dev_like(dst_idx, "dst_idx", dev, _I32, (pairs,)),
+                               _dev_like(status, "status", dev, _I32), _raw_stream(dev))
     _check(st, "ssm_pool_copy")
 
 
@@ -943,9 +947,9 @@ def ssm_pool_zero(pools, row_idx, status=None, stream=None) -> None:
     """Rows row_idx (int32 [n]; negative: skipped) of every pool <- 0."""
     arr, n, slots, like = _pools(pools)
     with _scope(like, stream):
-        _dev_like(row_idx, "row_idx", like, torch.int32)
-        _dev_like(status, "status", like, torch.int32)
-        st = lib.ssm_pool_zero(n, arr, slots, row_idx.numel(), _ptr(row_idx), _ptr(status), _stream(None))
+        dev, rows = like.get_device(), row_idx.shape[0]
+        st = lib.ssm_pool_zero(n, arr, slots, rows, _dev_like(row_idx, "row_idx", dev, _I32, (rows,)),
+                               _dev_like(status, "status", dev, _I32), _raw_stream(dev))
     _check(st, "ssm_pool_zero")
 
 
@@ -955,13 +959,13 @@ def ssm_pool_compact(pools, slot_idx, status=None, stream=None, workspace="auto"
     an int32 scalar tensor."""
     arr, n, slots, like = _pools(pools)
     with _scope(like, stream):
-        _dev_like(slot_idx, "slot_idx", like, torch.int32)
-        _dev_like(status, "status", like, torch.int32)
-        live = torch.empty((), dtype=torch.int32, device=like.device)
-        workspace = _workspace(
-            workspace, lambda: lib.ssm_pool_compact_workspace_size(slots, slot_idx.numel()), like)
-        st = lib.ssm_pool_compact(n, arr, slots, slot_idx.numel(), _ptr(slot_idx), _ptr(live),
-                                  _ptr(workspace), _bytes(workspace), _ptr(status), _stream(None))
+        dev, rows = like.get_device(), slot_idx.shape[0]
+        live = slot_idx.new_empty(())
+        size = lib.ssm_pool_compact_workspace_size(slots, rows) if workspace == "auto" else 0
+        ws, ws_ptr, ws_bytes = _workspace(workspace, size, like, dev)
+        st = lib.ssm_pool_compact(n, arr, slots, rows, _dev_like(slot_idx, "slot_idx", dev, _I32, (rows,)),
+                                  live.data_ptr(), ws_ptr, ws_bytes, _dev_like(status, "status", dev, _I32),
+                                  _raw_stream(dev))
     _check(st, "ssm_pool_compact")
     return live
 
