@@ -11,15 +11,18 @@
 // gradient of the final conv state (copies of the last K-1 inputs) adds to
 // the inputs it copies.
 //
-// A thread owns kCh adjacent channels and a tile of tokens.  It walks the tile
-// forward, recomputing pre from a register window of inputs; a second window
-// holds the last K-1 dpre, so din of token t is complete K-1 tokens later.
-// The tile's first K-1 and last K-1 tokens depend on its neighbours: the walk
+// A thread owns two adjacent channels (packed fp32 arithmetic) and a tile of
+// tokens, which it walks in groups of kGroup: the group's inputs and dy are
+// loaded together, one group ahead, so that 2 kGroup loads are in flight while
+// a group is computed.  pre comes from a register window of inputs; a second
+// window holds dpre, so din of token t is complete K-1 tokens later.  The
+// tile's first K-1 and last K-1 tokens depend on its neighbours: the walk
 // starts with the inputs of the K-1 tokens before the tile and runs K-1 tokens
-// past its end, recomputing their dpre (2 (K-1) of `kTile` tokens are read
-// twice, from L2).  Weight and bias sums stay in registers over the tile and
-// are added up over the tiles by a second launch, in a fixed order.
-// Bound by HBM: x and dy read once, dx written once.
+// past its end, recomputing their dpre (2 (K-1) of 128 tokens are read twice,
+// from L2).  A tile is 128 - (K-1) tokens, so that a walk inside one sequence
+// is a whole number of groups.  Weight and bias sums stay in registers over
+// the tile and are added up over the tiles by a second launch, in a fixed
+// order.  Bound by HBM: x and dy read once, dx written once.
 #include "selective.cuh"
 
 namespace ssm {
@@ -27,59 +30,60 @@ namespace ssm {
 namespace {
 
 constexpr int kBwdThreads = 128;
-constexpr int kTile = 128;
+constexpr int kGroup = 8;
 
-// Loads and stores of kCh adjacent channels.
-template <typename T, int kCh>
-__device__ __forceinline__ void load_ch(const T *p, float (&v)[kCh]) {
-    if constexpr (kCh == 1) {
-        v[0] = load_f32(p);
-    } else if constexpr (sizeof(T) == 2) {
-        const uint32_t q = __ldg(reinterpret_cast<const uint32_t *>(p));
-        v[0] = __uint_as_float(q << 16);
-        v[1] = __uint_as_float(q & 0xffff0000u);
+constexpr int tile_tokens(int K) { return 128 - (K - 1); }
+
+// Raw values of channels c, c + 1 of a row (the second only where it exists).
+template <typename T, bool kPair>
+__device__ __forceinline__ void load_two(const T *row, int c, bool both, uint32_t (&r)[2]) {
+    if constexpr (kPair) {
+        pair_load(row, c, r);
     } else {
-        const float2 q = __ldg(reinterpret_cast<const float2 *>(p));
-        v[0] = q.x;
-        v[1] = q.y;
+        r[0] = raw_load<T>(row, c);
+        r[1] = both ? raw_load<T>(row, c + 1) : 0u;
     }
 }
-template <typename T, int kCh>
-__device__ __forceinline__ void store_ch(T *p, const float (&v)[kCh]) {
-    if constexpr (kCh == 1) {
-        store_out(p, v[0]);
-    } else if constexpr (sizeof(T) == 2) {
-        *reinterpret_cast<__nv_bfloat162 *>(p) = __floats2bfloat162_rn(v[0], v[1]);
+template <typename T, bool kPair>
+__device__ __forceinline__ void store_two(T *row, int c, bool both, f32x2 v) {
+    if constexpr (kPair && sizeof(T) == 2) {
+        *reinterpret_cast<__nv_bfloat162 *>(row + c) = __floats2bfloat162_rn(lo2(v), hi2(v));
+    } else if constexpr (kPair) {
+        *reinterpret_cast<float2 *>(row + c) = make_float2(lo2(v), hi2(v));
     } else {
-        *reinterpret_cast<float2 *>(p) = make_float2(v[0], v[1]);
+        store_out(row + c, lo2(v));
+        if (both) store_out(row + c + 1, hi2(v));
     }
 }
 
-template <typename T, int K, int kCh>
+// kPair: dim is even, so two channels are one aligned access.
+template <typename T, int K, bool kPair>
 __global__ void __launch_bounds__(kBwdThreads)
 conv1d_bwd_kernel(ConvBwdArgs a, int ctiles)
 {
     constexpr int H = K - 1;                  // history entries
-    const int c = ((int)(blockIdx.x % ctiles) * kBwdThreads + threadIdx.x) * kCh;
+    const int c = ((int)(blockIdx.x % ctiles) * kBwdThreads + threadIdx.x) * 2;
     const long tile = blockIdx.x / ctiles;
     const long total = a.cu_seqlens ? (long)a.seqlen : (long)a.nseq * a.seqlen;
-    const long t0 = tile * kTile, t1 = min(t0 + kTile, total);
+    const long t0 = tile * tile_tokens(K), t1 = min(t0 + tile_tokens(K), total);
     if (c >= a.dim) return;
+    const bool both = kPair || c + 1 < a.dim;
+    const int c1 = both ? c + 1 : c;
     const T *x = static_cast<const T *>(a.x), *dy = static_cast<const T *>(a.dy);
     const T *init = static_cast<const T *>(a.initial), *dfin = static_cast<const T *>(a.dfinal);
     T *dx = static_cast<T *>(a.dx), *dinit = static_cast<T *>(a.dinitial);
 
-    float w[K][kCh], bias[kCh], dw[K][kCh], db[kCh];
+    f32x2 w[K], dw[K], db = pack2(0.f, 0.f);
 #pragma unroll
-    for (int q = 0; q < kCh; ++q) {
-#pragma unroll
-        for (int k = 0; k < K; ++k) {
-            w[k][q] = a.weight[(long)(c + q) * K + k];
-            dw[k][q] = 0.f;
-        }
-        bias[q] = a.bias ? a.bias[c + q] : 0.f;
-        db[q] = 0.f;
+    for (int k = 0; k < K; ++k) {
+        w[k] = pack2(a.weight[(long)c * K + k], a.weight[(long)c1 * K + k]);
+        dw[k] = db;
     }
+    const f32x2 bias = a.bias ? pack2(a.bias[c], a.bias[c1]) : db, one = pack2(1.f, 1.f);
+    // history entry h of sequence s
+    auto history = [&](const T *p, int s, long h) {
+        return pack2(load_f32(p + ((long)s * a.dim + c) * H + h), load_f32(p + ((long)s * a.dim + c1) * H + h));
+    };
 
     // sequence of the first token (the last s that starts at or before it)
     int s = 0;
@@ -113,93 +117,87 @@ conv1d_bwd_kernel(ConvBwdArgs a, int ctiles)
             ++s;
             continue;
         }
-        // win[k]: input of tap k of the current token (win[K-1] its own);
-        // dp[k]: dpre of token t-(K-1)+k
-        float win[K][kCh], dp[K][kCh];
+        const int nend = (int)(end - t);                        // tokens of this walk
+        const int npast = (int)(min(hi, end + H) - t);          // tokens whose dpre it needs
+        const T *xt = x + t * a.dim, *gt = dy + t * a.dim;
+        // win[H + i], dp[H + i]: input and dpre of token i of the group; the first H are the tokens before
+        f32x2 win[H + kGroup], dp[H + kGroup];
 #pragma unroll
-        for (int k = 0; k < K; ++k)
+        for (int k = 0; k < H; ++k) {
+            dp[k] = pack2(0.f, 0.f);
+            const long i = t - H + k;
+            uint32_t r[2] = {0u, 0u};
+            if (i >= lo) load_two<T, kPair>(x + i * a.dim, c, both, r);
+            win[k] = pair_value<T>(r);
+            if (i < lo && init && i >= lo - H) win[k] = history(init, s, i - lo + H);
+        }
+        uint32_t rx[kGroup][2], rg[kGroup][2];
+        auto fetch = [&](int i0) {
 #pragma unroll
-            for (int q = 0; q < kCh; ++q) win[k][q] = dp[k][q] = 0.f;
-        // entry i of the sequence's line: a token, or one of the H history entries before it
-        auto entry = [&](long i, float (&v)[kCh]) {
-            if (i >= lo) {
-                load_ch<T, kCh>(x + i * a.dim + c, v);
-            } else {
-#pragma unroll
-                for (int q = 0; q < kCh; ++q)
-                    v[q] = init && i >= lo - H ? load_f32(init + ((long)s * a.dim + c + q) * H + (i - lo + H)) : 0.f;
+            for (int i = 0; i < kGroup; ++i) {
+                rx[i][0] = rx[i][1] = rg[i][0] = rg[i][1] = 0u;
+                if (i0 + i < npast) {
+                    load_two<T, kPair>(xt + (long)(i0 + i) * a.dim, c, both, rx[i]);
+                    load_two<T, kPair>(gt + (long)(i0 + i) * a.dim, c, both, rg[i]);
+                }
             }
         };
+        fetch(0);
+        for (int i0 = 0; i0 < nend + H; i0 += kGroup) {
+            f32x2 g[kGroup];
 #pragma unroll
-        for (int k = 1; k < K; ++k) entry(t - K + k, win[k]);
-        const long past = min(hi, end + H);     // dpre is needed for H tokens past the end
-        for (long i = t; i < end + H; ++i) {
+            for (int i = 0; i < kGroup; ++i) {
+                win[H + i] = pair_value<T>(rx[i]);
+                g[i] = pair_value<T>(rg[i]);
+            }
+            if (i0 + kGroup < npast) fetch(i0 + kGroup);
 #pragma unroll
-            for (int k = 0; k + 1 < K; ++k)
+            for (int i = 0; i < kGroup; ++i) {
+                if (a.activation) {
+                    f32x2 pre = bias;
 #pragma unroll
-                for (int q = 0; q < kCh; ++q) {
-                    win[k][q] = win[k + 1][q];
-                    dp[k][q] = dp[k + 1][q];
+                    for (int k = 0; k < K; ++k) pre = fma2(w[k], win[i + k], pre);
+                    const f32x2 d = add2(ex2_pair(mul2(pre, pack2(-kLog2e, -kLog2e))), one);
+                    const f32x2 sg = pack2(rcp_approx(lo2(d)), rcp_approx(hi2(d)));
+                    g[i] = mul2(mul2(g[i], sg), fma2(pre, fma2(sg, pack2(-1.f, -1.f), one), one));
                 }
+                // tokens behind the sequence have no dpre (their g is zero, their pre need not be finite)
+                dp[H + i] = i0 + i < npast ? g[i] : pack2(0.f, 0.f);
+                if (i0 + i < nend) {
+                    db = add2(db, dp[H + i]);
 #pragma unroll
-            for (int q = 0; q < kCh; ++q) dp[K - 1][q] = 0.f;
-            if (i < past) {
-                float g[kCh];
-                load_ch<T, kCh>(x + i * a.dim + c, win[K - 1]);
-                load_ch<T, kCh>(dy + i * a.dim + c, g);
-#pragma unroll
-                for (int q = 0; q < kCh; ++q) {
-                    if (a.activation) {
-                        float pre = bias[q];
-#pragma unroll
-                        for (int k = 0; k < K; ++k) pre = fmaf(w[k][q], win[k][q], pre);
-                        const float sg = rcp_approx(1.f + ex2_approx(-pre * kLog2e));
-                        g[q] *= sg * fmaf(pre, 1.f - sg, 1.f);
-                    }
-                    dp[K - 1][q] = g[q];
+                    for (int k = 0; k < K; ++k) dw[k] = fma2(dp[H + i], win[i + k], dw[k]);
                 }
-                if (i < end) {
+                // entry i0 + i - H of the walk is complete: taps K-1 .. 0 read it
+                const int e = i0 + i - H;
+                if (e >= nend || (e < 0 && t != lo)) continue;    // another tile writes it
+                f32x2 din = mul2(w[K - 1], dp[i]);
 #pragma unroll
-                    for (int q = 0; q < kCh; ++q) {
-                        db[q] += g[q];
-#pragma unroll
-                        for (int k = 0; k < K; ++k) dw[k][q] = fmaf(g[q], win[k][q], dw[k][q]);
-                    }
+                for (int k = 1; k < K; ++k) din = fma2(w[K - 1 - k], dp[i + k], din);
+                const long at = t + e;
+                if (dfin && at >= hi - H) din = add2(din, history(dfin, s, at - hi + H));   // its copy in the final state
+                if (e >= 0) {
+                    store_two<T, kPair>(dx + at * a.dim, c, both, din);
+                } else if (dinit) {
+                    store_out(dinit + ((long)s * a.dim + c) * H + (e + H), lo2(din));
+                    if (both) store_out(dinit + ((long)s * a.dim + c1) * H + (e + H), hi2(din));
                 }
             }
-            // entry i - H of the line is complete: taps K-1 .. 0 read it at tokens i-H .. i
-            const long e = i - H;
-            if (e < t && !(t == lo)) continue;      // the tile before writes it
-            float din[kCh];
 #pragma unroll
-            for (int q = 0; q < kCh; ++q) {
-                din[q] = 0.f;
-#pragma unroll
-                for (int k = 0; k < K; ++k) din[q] = fmaf(w[K - 1 - k][q], dp[k][q], din[q]);
-            }
-            if (dfin && e >= hi - H) {              // the final conv state is a copy of it
-#pragma unroll
-                for (int q = 0; q < kCh; ++q)
-                    din[q] += load_f32(dfin + ((long)s * a.dim + c + q) * H + (e - hi + H));
-            }
-            if (e >= lo) {
-                store_ch<T, kCh>(dx + e * a.dim + c, din);
-            } else if (dinit) {
-#pragma unroll
-                for (int q = 0; q < kCh; ++q)
-                    store_out(dinit + ((long)s * a.dim + c + q) * H + (e - lo + H), din[q]);
+            for (int k = 0; k < H; ++k) {
+                win[k] = win[kGroup + k];
+                dp[k] = dp[kGroup + k];
             }
         }
         t = end;
     }
 
-    if (!a.part) return;
-    float *part = a.part + tile * (K + 1) * a.dim + c;
+    float *part = a.part + tile * (K + 1) * a.dim;
 #pragma unroll
-    for (int q = 0; q < kCh; ++q) {
-#pragma unroll
-        for (int k = 0; k < K; ++k) part[(long)k * a.dim + q] = dw[k][q];
-        part[(long)K * a.dim + q] = db[q];
+    for (int k = 0; k <= K; ++k) {
+        const f32x2 v = k < K ? dw[k < K ? k : 0] : db;
+        part[(long)k * a.dim + c] = lo2(v);
+        if (both) part[(long)k * a.dim + c1] = hi2(v);
     }
 }
 
@@ -242,16 +240,14 @@ conv1d_bwd_sum_kernel(ConvBwdArgs a, long tiles)
 template <typename T, int K>
 cudaError_t launch_k(const ConvBwdArgs &a, cudaStream_t stream)
 {
-    const long T_ = a.cu_seqlens ? (long)a.seqlen : (long)a.nseq * a.seqlen;
-    const long tiles = (T_ + kTile - 1) / kTile;
+    const long total = a.cu_seqlens ? (long)a.seqlen : (long)a.nseq * a.seqlen;
+    const long tiles = (total + tile_tokens(K) - 1) / tile_tokens(K);
     if (tiles > 0) {
-        // pairs of channels need an even row length for aligned pair accesses
-        const int ch = a.dim % 2 == 0 ? 2 : 1;
-        const int ctiles = (a.dim + kBwdThreads * ch - 1) / (kBwdThreads * ch);
+        const int ctiles = (a.dim + 2 * kBwdThreads - 1) / (2 * kBwdThreads);
         if (tiles * ctiles > 0x7fffffffL) return cudaErrorInvalidValue;
         const unsigned blocks = (unsigned)(tiles * ctiles);
-        if (ch == 2) conv1d_bwd_kernel<T, K, 2><<<blocks, kBwdThreads, 0, stream>>>(a, ctiles);
-        else conv1d_bwd_kernel<T, K, 1><<<blocks, kBwdThreads, 0, stream>>>(a, ctiles);
+        if (a.dim % 2 == 0) conv1d_bwd_kernel<T, K, true><<<blocks, kBwdThreads, 0, stream>>>(a, ctiles);
+        else conv1d_bwd_kernel<T, K, false><<<blocks, kBwdThreads, 0, stream>>>(a, ctiles);
     }
     if (a.dinitial && K > 1) conv1d_bwd_empty_kernel<T><<<(unsigned)a.nseq, 256, 0, stream>>>(a);
     conv1d_bwd_sum_kernel<<<dim3((unsigned)((a.dim + 31) / 32), (unsigned)(K + 1)), 1024, 0, stream>>>(a, tiles);
@@ -277,7 +273,8 @@ cudaError_t launch_t(const ConvBwdArgs &a, cudaStream_t stream)
 
 size_t conv1d_bwd_workspace(long T, int dim, int width)
 {
-    return (size_t)((T + kTile - 1) / kTile) * (width + 1) * dim * sizeof(float);
+    const long n = tile_tokens(width);
+    return (size_t)((T + n - 1) / n) * (width + 1) * dim * sizeof(float);
 }
 
 cudaError_t launch_conv1d_bwd(const ConvBwdArgs &a, cudaStream_t stream)
