@@ -215,6 +215,7 @@ int selective_scan_bwd(int nseq, int seqlen, const int32_t *cu_seqlens, int dim,
     a.x_stride = x_stride; a.dt_stride = dt_stride; a.B_stride = B_stride; a.C_stride = C_stride; a.z_stride = z_stride;
     a.A = A; a.D = D; a.dtp = dtp;
     a.saved = const_cast<float *>(saved_states);
+    a.pairs = dim / ngroups % 2 == 0 && paired(rows[0]) && paired(rows[1]) && paired(rows[4]) && paired(rows[5]);
     a.status_dev = status_dev;
     b.dy = dy; b.dy_stride = dy_stride; b.dfinal = dfinal_state;
     b.dx = dx; b.ddt = ddt; b.dA = dA; b.dB = dB; b.dC = dC; b.dD = dD; b.dz = dz;
@@ -276,7 +277,7 @@ int causal_conv1d_bwd(int nseq, int seqlen, const int32_t *cu_seqlens, int dim, 
 {
     if (nseq < 0 || seqlen < 0 || dim <= 0 || width < 1) return SSM_ERR_INVALID_ARG;
     if (!valid_dtype(in_dtype) || (activation != 0 && activation != 1)) return SSM_ERR_INVALID_ARG;
-    if (width > 8 || nseq > 0x7fffffff / 2) return SSM_ERR_UNSUPPORTED;
+    if (width > 8 || nseq > 0x7fffffff / 2 || dim > kMaxRow / 2) return SSM_ERR_UNSUPPORTED;
     if (cu_seqlens && nseq == 0 && seqlen != 0) return SSM_ERR_INVALID_ARG;
     const long long T = tokens_of(nseq, seqlen, cu_seqlens);
     if (T > 0x7fffffffLL) return SSM_ERR_UNSUPPORTED;

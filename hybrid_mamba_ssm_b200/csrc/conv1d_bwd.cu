@@ -58,7 +58,7 @@ __device__ __forceinline__ void store_two(T *row, int c, bool both, f32x2 v) {
 
 // kPair: dim is even, so two channels are one aligned access.
 template <typename T, int K, bool kPair>
-__global__ void __launch_bounds__(kBwdThreads)
+__global__ void __launch_bounds__(kBwdThreads, K <= 4 ? 4 : 3)
 conv1d_bwd_kernel(ConvBwdArgs a, int ctiles)
 {
     constexpr int H = K - 1;                  // history entries
@@ -119,7 +119,10 @@ conv1d_bwd_kernel(ConvBwdArgs a, int ctiles)
         }
         const int nend = (int)(end - t);                        // tokens of this walk
         const int npast = (int)(min(hi, end + H) - t);          // tokens whose dpre it needs
+        const int start = t == lo ? -H : 0;                     // first entry that this walk completes
+        const int copied = dfin ? (int)min(hi - H - t, (long)nend) : nend;   // entries from here on are in the final state
         const T *xt = x + t * a.dim, *gt = dy + t * a.dim;
+        T *ot = dx + t * a.dim;
         // win[H + i], dp[H + i]: input and dpre of token i of the group; the first H are the tokens before
         f32x2 win[H + kGroup], dp[H + kGroup];
 #pragma unroll
@@ -132,15 +135,47 @@ conv1d_bwd_kernel(ConvBwdArgs a, int ctiles)
             if (i < lo && init && i >= lo - H) win[k] = history(init, s, i - lo + H);
         }
         uint32_t rx[kGroup][2], rg[kGroup][2];
-        auto fetch = [&](int i0) {
+        auto fetch = [&](int i0) {                              // 32-bit offsets from the walk's first row
+            if (i0 + kGroup <= npast) {
 #pragma unroll
-            for (int i = 0; i < kGroup; ++i) {
-                rx[i][0] = rx[i][1] = rg[i][0] = rg[i][1] = 0u;
-                if (i0 + i < npast) {
-                    load_two<T, kPair>(xt + (long)(i0 + i) * a.dim, c, both, rx[i]);
-                    load_two<T, kPair>(gt + (long)(i0 + i) * a.dim, c, both, rg[i]);
+                for (int i = 0; i < kGroup; ++i) {
+                    load_two<T, kPair>(xt, (i0 + i) * a.dim + c, both, rx[i]);
+                    load_two<T, kPair>(gt, (i0 + i) * a.dim + c, both, rg[i]);
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < kGroup; ++i) {
+                    rx[i][0] = rx[i][1] = rg[i][0] = rg[i][1] = 0u;
+                    if (i0 + i < npast) {
+                        load_two<T, kPair>(xt, (i0 + i) * a.dim + c, both, rx[i]);
+                        load_two<T, kPair>(gt, (i0 + i) * a.dim + c, both, rg[i]);
+                    }
                 }
             }
+        };
+        // gradient through the activation, for the group's tokens
+        auto group_dpre = [&](f32x2 (&g)[kGroup]) {
+            if (!a.activation) return;
+#pragma unroll
+            for (int i = 0; i < kGroup; ++i) {
+                f32x2 pre = bias;
+#pragma unroll
+                for (int k = 0; k < K; ++k) pre = fma2(w[k], win[i + k], pre);
+                const f32x2 d = add2(ex2_pair(mul2(pre, pack2(-kLog2e, -kLog2e))), one);
+                const f32x2 sg = pack2(rcp_approx(lo2(d)), rcp_approx(hi2(d)));
+                g[i] = mul2(mul2(g[i], sg), fma2(pre, fma2(sg, pack2(-1.f, -1.f), one), one));
+            }
+        };
+        auto add_weight = [&](int i) {                          // token i of the group in the sums
+            db = add2(db, dp[H + i]);
+#pragma unroll
+            for (int k = 0; k < K; ++k) dw[k] = fma2(dp[H + i], win[i + k], dw[k]);
+        };
+        auto taps = [&](int i) {                                // din of the entry H tokens before it
+            f32x2 din = mul2(w[K - 1], dp[i]);
+#pragma unroll
+            for (int k = 1; k < K; ++k) din = fma2(w[K - 1 - k], dp[i + k], din);
+            return din;
         };
         fetch(0);
         for (int i0 = 0; i0 < nend + H; i0 += kGroup) {
@@ -151,36 +186,30 @@ conv1d_bwd_kernel(ConvBwdArgs a, int ctiles)
                 g[i] = pair_value<T>(rg[i]);
             }
             if (i0 + kGroup < npast) fetch(i0 + kGroup);
+            group_dpre(g);
+            if (i0 >= H && i0 + kGroup <= nend && i0 + kGroup - H <= copied) {   // all inside: no conditions
 #pragma unroll
-            for (int i = 0; i < kGroup; ++i) {
-                if (a.activation) {
-                    f32x2 pre = bias;
-#pragma unroll
-                    for (int k = 0; k < K; ++k) pre = fma2(w[k], win[i + k], pre);
-                    const f32x2 d = add2(ex2_pair(mul2(pre, pack2(-kLog2e, -kLog2e))), one);
-                    const f32x2 sg = pack2(rcp_approx(lo2(d)), rcp_approx(hi2(d)));
-                    g[i] = mul2(mul2(g[i], sg), fma2(pre, fma2(sg, pack2(-1.f, -1.f), one), one));
+                for (int i = 0; i < kGroup; ++i) {
+                    dp[H + i] = g[i];
+                    add_weight(i);
+                    store_two<T, kPair>(ot, (i0 + i - H) * a.dim + c, both, taps(i));
                 }
-                // tokens behind the sequence have no dpre (their g is zero, their pre need not be finite)
-                dp[H + i] = i0 + i < npast ? g[i] : pack2(0.f, 0.f);
-                if (i0 + i < nend) {
-                    db = add2(db, dp[H + i]);
+            } else {
 #pragma unroll
-                    for (int k = 0; k < K; ++k) dw[k] = fma2(dp[H + i], win[i + k], dw[k]);
-                }
-                // entry i0 + i - H of the walk is complete: taps K-1 .. 0 read it
-                const int e = i0 + i - H;
-                if (e >= nend || (e < 0 && t != lo)) continue;    // another tile writes it
-                f32x2 din = mul2(w[K - 1], dp[i]);
-#pragma unroll
-                for (int k = 1; k < K; ++k) din = fma2(w[K - 1 - k], dp[i + k], din);
-                const long at = t + e;
-                if (dfin && at >= hi - H) din = add2(din, history(dfin, s, at - hi + H));   // its copy in the final state
-                if (e >= 0) {
-                    store_two<T, kPair>(dx + at * a.dim, c, both, din);
-                } else if (dinit) {
-                    store_out(dinit + ((long)s * a.dim + c) * H + (e + H), lo2(din));
-                    if (both) store_out(dinit + ((long)s * a.dim + c1) * H + (e + H), hi2(din));
+                for (int i = 0; i < kGroup; ++i) {
+                    // tokens behind the sequence have no dpre (their pre need not be finite)
+                    dp[H + i] = i0 + i < npast ? g[i] : pack2(0.f, 0.f);
+                    if (i0 + i < nend) add_weight(i);
+                    const int e = i0 + i - H;
+                    if (e >= nend || e < start) continue;       // another walk completes it
+                    f32x2 din = taps(i);
+                    if (e >= copied) din = add2(din, history(dfin, s, t + e - hi + H));
+                    if (e >= 0) {
+                        store_two<T, kPair>(ot, e * a.dim + c, both, din);
+                    } else if (dinit) {
+                        store_out(dinit + ((long)s * a.dim + c) * H + (e + H), lo2(din));
+                        if (both) store_out(dinit + ((long)s * a.dim + c1) * H + (e + H), hi2(din));
+                    }
                 }
             }
 #pragma unroll

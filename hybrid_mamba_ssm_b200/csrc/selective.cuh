@@ -140,11 +140,13 @@ __device__ __forceinline__ float dt_value(const DtParams &p, float raw, float bi
 __device__ __forceinline__ float dt_slope(const DtParams &p, float raw, float bias) {
     float v = raw + bias, d = 1.f;
     if (p.softplus) {
-        const float e = exp_neg(min_nan(fabsf(v), 120.f)), r = rcp_approx(1.f + e);
+        const float e = ex2_approx(min_nan(fabsf(v), 120.f) * -kLog2e), r = rcp_approx(1.f + e);
         d = v >= 0.f ? r : e * r;
-        v = fmaxf(v, 0.f) + log1p_unit(e);
     }
-    if (p.clamp && (v < p.lo || v > p.hi)) d = 0.f;
+    if (p.clamp) {
+        if (p.softplus) v = fmaxf(v, 0.f) + log1p_unit(exp_neg(min_nan(fabsf(v), 120.f)));
+        if (v < p.lo || v > p.hi) d = 0.f;
+    }
     return d;
 }
 

@@ -21,10 +21,13 @@
 // L lanes share a channel, each with R states in packed pairs; a warp holds
 // 32 / L channels at a time and takes CS such sets one after another, adding
 // their dB and dC in registers before they are summed over its channels by
-// shuffles (the sums over n, three per token and channel, go over the L lanes
-// of a channel).  Per sub-tile the CTA's warps are added up through shared
-// memory and the sum is written as one part per channel tile; a second launch
-// adds the parts, in a fixed order, so results do not depend on the schedule.
+// shuffles.  The sums over n (three per token and channel) go over the L lanes
+// of a channel and end with the sub-tile's tokens spread over those lanes:
+// each lane then finishes its tokens' dx, ddt and dz from the inputs, which it
+// loaded when the sub-tile began.  Per sub-tile the CTA's warps are added up
+// through shared memory and the sum is written as one part per channel tile; a
+// second launch adds the parts, in a fixed order, so results do not depend on
+// the schedule.
 #include "selective.cuh"
 
 namespace ssm {
@@ -43,13 +46,26 @@ struct BwdShape {
     static constexpr int CW = CL * CS;           // channels of a warp
     static constexpr int CB = CW * kWarps;       // channels of a CTA
     static constexpr int NP = R * L;
+    // floats of shared memory: v and v x, gated dy; B, C; sub-tile states; parts of dB, dC (two buffers)
     static constexpr int kRow = kSavedEvery * CB;
-    // floats of shared memory: v, u, g; B, C; sub-tile states; parts of dB, dC (two buffers)
     static constexpr int kStates = kSubs * CS * kBwdThreads * R;
     static constexpr int kParts = 2 * 2 * kWarps * kSub * NP;
     static constexpr size_t kBytes = sizeof(float) * (3 * kRow + 2 * kSavedEvery * NP + kStates + kParts);
-    static_assert(kBwdThreads % CB == 0, "a staging thread keeps its channel");
+    static_assert(CB % 2 == 0 && kBwdThreads % (CB / 2) == 0, "a staging thread keeps its two channels");
 };
+
+// First value that reduce_lanes<TG, S, kLow> leaves in this lane.
+template <int TG, int S, int kLow>
+__device__ __forceinline__ int reduced_first(int lane) {
+    int first = 0, n = TG;
+#pragma unroll
+    for (int o = kLow * S / 2; o >= kLow; o >>= 1)
+        if (n > 1) {
+            n /= 2;
+            if (lane & o) first += n;
+        }
+    return first;
+}
 
 template <int R>
 __device__ __forceinline__ void load_row(const float *row, int j, int N, f32x2 (&h)[R / 2]) {
@@ -80,15 +96,17 @@ __device__ __forceinline__ void store_row(float *row, int j, int N, const f32x2 
 }
 
 template <typename TIn, typename TDt, int R, int L, int CS>
-__global__ void __launch_bounds__(kBwdThreads)
+__global__ void __launch_bounds__(kBwdThreads, R == 4 ? 3 : 1)
 selective_scan_bwd_kernel(SelScanBwdArgs b, int units)
 {
     using S = BwdShape<R, L, CS>;
-    constexpr int CB = S::CB, NP = S::NP, P = R / 2, KC = kSavedEvery;
-    constexpr int RS = kBwdThreads / CB;         // tokens per staging step
+    constexpr int CB = S::CB, CL = S::CL, NP = S::NP, P = R / 2, KC = kSavedEvery;
+    constexpr int RS = kBwdThreads / (CB / 2);       // tokens per staging step (a thread: two channels)
+    constexpr int kLeft = reduce_left(kSub, L);      // tokens of a sub-tile that a lane finishes
+    constexpr int kSame = L > kSub ? L / kSub : 1;   // lanes that end with the same sums
     extern __shared__ __align__(16) float smem[];
-    float *s_v = smem, *s_u = s_v + S::kRow, *s_g = s_u + S::kRow;
-    float *s_B = s_g + S::kRow, *s_C = s_B + KC * NP;
+    float2 *s_vu = reinterpret_cast<float2 *>(smem);
+    float *s_g = smem + 2 * S::kRow, *s_B = s_g + S::kRow, *s_C = s_B + KC * NP;
     float *s_h = s_C + KC * NP, *s_part = s_h + S::kStates;
     const SelScanArgs &a = b.f;
 
@@ -101,23 +119,27 @@ selective_scan_bwd_kernel(SelScanBwdArgs b, int units)
     const long T = a.cu_seqlens ? (long)a.seqlen : (long)a.nseq * a.seqlen;
 
     const int j = lane % L;
-    const int ch0 = warp * S::CW + lane / L;     // channel of set q: ch0 + q * CL
-    const int sc = tid % CB, st = tid / CB, ds = c0 + sc;
-    const bool slive = ds < cend;
-    const float bias = slive && a.dtp.bias ? a.dtp.bias[ds] : 0.f;
-    const float skip = slive && a.D ? a.D[ds] : 0.f;
+    const int ch0 = warp * S::CW + lane / L;         // channel of set q: c0 + ch0 + q * CL
+    const int first = reduced_first<kSub, L, 1>(lane);
+    const int sc = 2 * (tid % (CB / 2)), st = tid / (CB / 2), ds = c0 + sc;   // staging: channels ds, ds + 1
+    const bool slive0 = ds < cend, slive1 = ds + 1 < cend;
+    const f32x2 bias2 = pack2(a.dtp.bias && slive0 ? a.dtp.bias[ds] : 0.f, a.dtp.bias && slive1 ? a.dtp.bias[ds + 1] : 0.f);
+    const int xs = (int)a.x_stride, vs = (int)a.dt_stride, ys = (int)b.dy_stride, zs = (int)a.z_stride;
+    const int Bs = (int)a.B_stride, Cs = (int)a.C_stride;
+    const bool whole_rows = a.pairs && cend - c0 == CB && N == NP;
 
     f32x2 A[CS][P], G[CS][P], dA[CS][P];
+    float sum_D[CS], sum_bias[CS];
 #pragma unroll
     for (int q = 0; q < CS; ++q) {
-        const int d = c0 + ch0 + q * S::CL;
+        const int d = c0 + ch0 + q * CL;
+        sum_D[q] = sum_bias[q] = 0.f;
 #pragma unroll
         for (int p = 0; p < P; ++p) A[q][p] = dA[q][p] = pack2(0.f, 0.f);
         if (d < cend) load_row<R>(a.A + (long)d * N, j, N, A[q]);
 #pragma unroll
         for (int p = 0; p < P; ++p) A[q][p] = mul2(A[q][p], pack2(kLog2e, kLog2e));
     }
-    float sum_D = 0.f, sum_bias = 0.f;
 
     for (int s = unit; s < a.nseq; s += units) {
         long lo, hi;
@@ -128,7 +150,7 @@ selective_scan_bwd_kernel(SelScanBwdArgs b, int units)
         const long save0 = lo / KC + s;
 #pragma unroll
         for (int q = 0; q < CS; ++q) {
-            const int d = c0 + ch0 + q * S::CL;
+            const int d = c0 + ch0 + q * CL;
 #pragma unroll
             for (int p = 0; p < P; ++p) G[q][p] = pack2(0.f, 0.f);
             if (b.dfinal && d < cend) load_row<R>(b.dfinal + ((long)s * a.dim + d) * N, j, N, G[q]);
@@ -137,57 +159,77 @@ selective_scan_bwd_kernel(SelScanBwdArgs b, int units)
         for (long chunk = (hi - lo + KC - 1) / KC - 1; chunk >= 0; --chunk) {
             const long t0 = lo + chunk * KC;
             const int n_tok = (int)min((long)KC, hi - t0);
+            // rows of the chunk's first token; everything below is a 32-bit offset from them
+            const TIn *xt = static_cast<const TIn *>(a.x) + t0 * xs + c0, *yt = static_cast<const TIn *>(b.dy) + t0 * ys + c0;
+            const TIn *zt = static_cast<const TIn *>(a.z) + t0 * zs + c0;
+            const TDt *vt = static_cast<const TDt *>(a.dt) + t0 * vs + c0;
+            const TIn *Bt = static_cast<const TIn *>(a.B) + t0 * Bs + grp * N, *Ct = static_cast<const TIn *>(a.C) + t0 * Cs + grp * N;
+            const bool full = whole_rows && n_tok == KC;
+
+            f32x2 h[CS][P];
+#pragma unroll
+            for (int q = 0; q < CS; ++q) {
+                const int d = c0 + ch0 + q * CL;
+#pragma unroll
+                for (int p = 0; p < P; ++p) h[q][p] = pack2(0.f, 0.f);
+                if (d < cend) load_row<R>(a.saved + ((save0 + chunk) * a.dim + d) * N, j, N, h[q]);
+            }
             // stage: step sizes, v x, gated dy; B, C; zero behind the sequence's end
-            constexpr int kStep = 4;             // tokens whose loads are in flight together
+            constexpr int kStep = KC / RS < 4 ? (KC / RS < 1 ? 1 : KC / RS) : 4;   // tokens whose loads are in flight together
+#pragma unroll 1
             for (int k0 = st; k0 < KC; k0 += RS * kStep) {
-                uint32_t rv[kStep], rx[kStep], rg[kStep], rz[kStep];
+                uint32_t rv[kStep][2], rx[kStep][2], rg[kStep][2], rz[kStep][2];
 #pragma unroll
                 for (int i = 0; i < kStep; ++i) {
                     const int k = k0 + i * RS;
-                    const long t = t0 + k;
-                    const bool ok = slive && k < n_tok;
-                    rv[i] = ok ? raw_load<TDt>(a.dt, t * a.dt_stride + ds) : 0u;
-                    rx[i] = ok ? raw_load<TIn>(a.x, t * a.x_stride + ds) : 0u;
-                    rg[i] = ok ? raw_load<TIn>(b.dy, t * b.dy_stride + ds) : 0u;
-                    rz[i] = ok && a.z ? raw_load<TIn>(a.z, t * a.z_stride + ds) : 0u;
+                    if (full) {
+                        pair_load(vt, k * vs + sc, rv[i]);
+                        pair_load(xt, k * xs + sc, rx[i]);
+                        pair_load(yt, k * ys + sc, rg[i]);
+                        if (a.z) pair_load(zt, k * zs + sc, rz[i]);
+                    } else {
+#pragma unroll
+                        for (int w = 0; w < 2; ++w) {
+                            const bool ok = k < n_tok && (w ? slive1 : slive0);
+                            rv[i][w] = ok ? raw_load<TDt>(vt, k * vs + sc + w) : 0u;
+                            rx[i][w] = ok ? raw_load<TIn>(xt, k * xs + sc + w) : 0u;
+                            rg[i][w] = ok ? raw_load<TIn>(yt, k * ys + sc + w) : 0u;
+                            rz[i][w] = ok && a.z ? raw_load<TIn>(zt, k * zs + sc + w) : 0u;
+                        }
+                    }
                 }
 #pragma unroll
                 for (int i = 0; i < kStep; ++i) {
                     const int k = k0 + i * RS;
-                    if (k >= KC) break;
-                    const float v = slive && k < n_tok ? dt_value(a.dtp, raw_value<TDt>(rv[i]), bias) : 0.f;
-                    float g = raw_value<TIn>(rg[i]);
-                    if (a.z) g *= silu_approx(raw_value<TIn>(rz[i]));
-                    s_v[k * CB + sc] = v;
-                    s_u[k * CB + sc] = v * raw_value<TIn>(rx[i]);
-                    s_g[k * CB + sc] = g;
+                    f32x2 v = dt_value2(a.dtp, pair_value<TDt>(rv[i]), bias2);
+                    if (k >= n_tok) v = pack2(0.f, 0.f);
+                    const f32x2 u = mul2(v, pair_value<TIn>(rx[i]));
+                    f32x2 g = pair_value<TIn>(rg[i]);
+                    if (a.z) g = mul2(g, silu2(pair_value<TIn>(rz[i])));
+                    if (KC % (RS * kStep) && k >= KC) break;
+                    *reinterpret_cast<float4 *>(&s_vu[k * CB + sc]) = make_float4(lo2(v), lo2(u), hi2(v), hi2(u));
+                    *reinterpret_cast<float2 *>(&s_g[k * CB + sc]) = make_float2(lo2(g), hi2(g));
                 }
             }
 #pragma unroll 4
             for (int e = tid; e < KC * NP; e += kBwdThreads) {
                 const int k = e / NP, n = e % NP;
                 const bool ok = k < n_tok && n < N;
-                s_B[e] = ok ? ld_as<TIn>(a.B, (t0 + k) * a.B_stride + (long)grp * N + n) : 0.f;
-                s_C[e] = ok ? ld_as<TIn>(a.C, (t0 + k) * a.C_stride + (long)grp * N + n) : 0.f;
-            }
-            f32x2 h[CS][P];
-#pragma unroll
-            for (int q = 0; q < CS; ++q) {
-                const int d = c0 + ch0 + q * S::CL;
-#pragma unroll
-                for (int p = 0; p < P; ++p) h[q][p] = pack2(0.f, 0.f);
-                if (d < cend) load_row<R>(a.saved + ((save0 + chunk) * a.dim + d) * N, j, N, h[q]);
+                s_B[e] = ok ? ld_as<TIn>(Bt, k * Bs + n) : 0.f;
+                s_C[e] = ok ? ld_as<TIn>(Ct, k * Cs + n) : 0.f;
             }
             __syncthreads();
 
             const int last = (n_tok - 1) / kSub;
             // forward: the state in front of every sub-tile
+#pragma unroll 1
             for (int sub = 0; sub <= last; ++sub) {
 #pragma unroll
                 for (int q = 0; q < CS; ++q) {
                     float *slot = s_h + ((sub * CS + q) * kBwdThreads + tid) * R;
 #pragma unroll
-                    for (int p = 0; p < P; ++p) reinterpret_cast<unsigned long long *>(slot)[p] = h[q][p].v;
+                    for (int p = 0; p < P; p += 2)
+                        *reinterpret_cast<ulonglong2 *>(slot + 2 * p) = make_ulonglong2(h[q][p].v, h[q][p + 1].v);
                 }
                 if (sub == last) break;
 #pragma unroll
@@ -197,76 +239,99 @@ selective_scan_bwd_kernel(SelScanBwdArgs b, int units)
                     lds_pairs(s_B + t * NP + j * R, B);
 #pragma unroll
                     for (int q = 0; q < CS; ++q) {
-                        const float v = s_v[t * CB + ch0 + q * S::CL], u = s_u[t * CB + ch0 + q * S::CL];
+                        const float2 vu = s_vu[t * CB + ch0 + q * CL];
 #pragma unroll
                         for (int p = 0; p < P; ++p)
-                            h[q][p] = fma2(ex2_pair(mul2(pack2(v, v), A[q][p])), h[q][p], mul2(pack2(u, u), B[p]));
+                            h[q][p] = fma2(ex2_pair(mul2(pack2(vu.x, vu.x), A[q][p])), h[q][p], mul2(pack2(vu.y, vu.y), B[p]));
                     }
                 }
             }
 
+#pragma unroll 1
             for (int sub = last; sub >= 0; --sub) {
-                f32x2 dB[kSub][P], dC[kSub][P];
+                f32x2 dB[kSub][P], dC[kSub][P], B[kSub][P], C[kSub][P];
 #pragma unroll
-                for (int k = 0; k < kSub; ++k)
-#pragma unroll
-                    for (int p = 0; p < P; ++p) dB[k][p] = dC[k][p] = pack2(0.f, 0.f);
+                for (int k = 0; k < kSub; ++k) {
+                    lds_pairs(s_B + (sub * kSub + k) * NP + j * R, B[k]);
+                    lds_pairs(s_C + (sub * kSub + k) * NP + j * R, C[k]);
+                }
 #pragma unroll
                 for (int q = 0; q < CS; ++q) {
-                    const int ch = ch0 + q * S::CL;
+                    const int ch = ch0 + q * CL, d = c0 + ch;
+                    // inputs of the tokens that this lane finishes
+                    uint32_t rv[kLeft], rx[kLeft], rg[kLeft], rz[kLeft];
+                    bool mine[kLeft];
+#pragma unroll
+                    for (int i = 0; i < kLeft; ++i) {
+                        const int t = sub * kSub + first + i;
+                        mine[i] = t < n_tok && d < cend && j % kSame == 0;
+                        rv[i] = rx[i] = rg[i] = rz[i] = 0u;
+                        if (mine[i]) {
+                            rv[i] = raw_load<TDt>(vt, t * vs + ch);
+                            rx[i] = raw_load<TIn>(xt, t * xs + ch);
+                            if (a.z) {
+                                rg[i] = raw_load<TIn>(yt, t * ys + ch);
+                                rz[i] = raw_load<TIn>(zt, t * zs + ch);
+                            }
+                        }
+                    }
                     f32x2 hh[kSub + 1][P], aa[kSub][P];
                     lds_pairs(s_h + ((sub * CS + q) * kBwdThreads + tid) * R, hh[0]);
+                    float2 vu[kSub];
 #pragma unroll
                     for (int k = 0; k < kSub; ++k) {
-                        const int t = sub * kSub + k;
-                        const float v = s_v[t * CB + ch], u = s_u[t * CB + ch];
-                        f32x2 B[P];
-                        lds_pairs(s_B + t * NP + j * R, B);
+                        vu[k] = s_vu[(sub * kSub + k) * CB + ch];
 #pragma unroll
                         for (int p = 0; p < P; ++p) {
-                            aa[k][p] = ex2_pair(mul2(pack2(v, v), A[q][p]));
-                            hh[k + 1][p] = fma2(aa[k][p], hh[k][p], mul2(pack2(u, u), B[p]));
+                            aa[k][p] = ex2_pair(mul2(pack2(vu[k].x, vu[k].x), A[q][p]));
+                            hh[k + 1][p] = fma2(aa[k][p], hh[k][p], mul2(pack2(vu[k].y, vu[k].y), B[k][p]));
                         }
                     }
                     float yv[kSub], wv[kSub], qv[kSub];
 #pragma unroll
                     for (int k = kSub - 1; k >= 0; --k) {
-                        const int t = sub * kSub + k;
-                        const float v = s_v[t * CB + ch], u = s_u[t * CB + ch], g = s_g[t * CB + ch];
-                        const f32x2 vv = pack2(v, v), uu = pack2(u, u), gg = pack2(g, g);
-                        f32x2 B[P], C[P], ya = pack2(0.f, 0.f), wa = ya, qa = ya;
-                        lds_pairs(s_B + t * NP + j * R, B);
-                        lds_pairs(s_C + t * NP + j * R, C);
+                        const float g = s_g[(sub * kSub + k) * CB + ch];
+                        const f32x2 vv = pack2(vu[k].x, vu[k].x), uu = pack2(vu[k].y, vu[k].y), gg = pack2(g, g);
+                        f32x2 ya, wa, qa;
 #pragma unroll
                         for (int p = 0; p < P; ++p) {
-                            const f32x2 dh = fma2(gg, C[p], G[q][p]);
-                            ya = fma2(hh[k + 1][p], C[p], ya);
-                            dC[k][p] = fma2(hh[k + 1][p], gg, dC[k][p]);
-                            dB[k][p] = fma2(dh, uu, dB[k][p]);
-                            wa = fma2(dh, B[p], wa);
+                            const f32x2 dh = fma2(gg, C[k][p], G[q][p]);
                             G[q][p] = mul2(aa[k][p], dh);
                             const f32x2 qq = mul2(G[q][p], hh[k][p]);
-                            qa = fma2(qq, A[q][p], qa);
                             dA[q][p] = fma2(qq, vv, dA[q][p]);
+                            ya = p ? fma2(hh[k + 1][p], C[k][p], ya) : mul2(hh[k + 1][p], C[k][p]);
+                            wa = p ? fma2(dh, B[k][p], wa) : mul2(dh, B[k][p]);
+                            qa = p ? fma2(qq, A[q][p], qa) : mul2(qq, A[q][p]);
+                            dC[k][p] = q ? fma2(hh[k + 1][p], gg, dC[k][p]) : mul2(hh[k + 1][p], gg);
+                            dB[k][p] = q ? fma2(dh, uu, dB[k][p]) : mul2(dh, uu);
                         }
                         yv[k] = sum2(ya);
                         wv[k] = sum2(wa);
                         qv[k] = sum2(qa);
                     }
-                    const int first = reduce_lanes<kSub, L, 1>(yv, lane);
+                    reduce_lanes<kSub, L, 1>(yv, lane);
                     reduce_lanes<kSub, L, 1>(wv, lane);
                     reduce_lanes<kSub, L, 1>(qv, lane);
-                    constexpr int kLeft = reduce_left(kSub, L), kSame = L > kSub ? L / kSub : 1;
-                    __syncwarp();
-                    // the channel's lanes have read v, u, g of these tokens: the sums take their place
-                    if (j % kSame == 0) {
+                    const float bias = a.dtp.bias && d < cend ? __ldg(a.dtp.bias + d) : 0.f;
+                    const float skip = a.D && d < cend ? __ldg(a.D + d) : 0.f;
 #pragma unroll
-                        for (int i = 0; i < kLeft; ++i) {
-                            const int t = sub * kSub + first + i;
-                            s_v[t * CB + ch] = qv[i];
-                            s_u[t * CB + ch] = wv[i];
-                            s_g[t * CB + ch] = yv[i];
+                    for (int i = 0; i < kLeft; ++i) {
+                        if (!mine[i]) continue;
+                        const int t = sub * kSub + first + i;
+                        const long o = t0 * a.dim + c0;
+                        const int oo = t * a.dim + ch;
+                        const float x = raw_value<TIn>(rx[i]), v = s_vu[t * CB + ch].x, g = s_g[t * CB + ch];
+                        if (a.z) {
+                            const float z = raw_value<TIn>(rz[i]);
+                            const float sg = rcp_approx(1.f + ex2_approx(-z * kLog2e));
+                            store_out(static_cast<TIn *>(b.dz) + o + oo,
+                                      raw_value<TIn>(rg[i]) * fmaf(skip, x, yv[i]) * sg * fmaf(z, 1.f - sg, 1.f));
                         }
+                        const float ddt = fmaf(qv[i], kLn2, wv[i] * x) * dt_slope(a.dtp, raw_value<TDt>(rv[i]), bias);
+                        store_out(static_cast<TIn *>(b.dx) + o + oo, fmaf(wv[i], v, skip * g));
+                        store_out(static_cast<TDt *>(b.ddt) + o + oo, ddt);
+                        sum_D[q] = fmaf(g, x, sum_D[q]);
+                        sum_bias[q] += ddt;
                     }
                 }
                 // dB, dC of the sub-tile: over the warp's channels, then the CTA's warps
@@ -281,68 +346,34 @@ selective_scan_bwd_kernel(SelScanBwdArgs b, int units)
                             f[k * R + 2 * p] = w ? lo2(dC[k][p]) : lo2(dB[k][p]);
                             f[k * R + 2 * p + 1] = w ? hi2(dC[k][p]) : hi2(dB[k][p]);
                         }
-                    const int first = reduce_lanes<kSub * R, S::CL, L>(f, lane);
-                    constexpr int kLeft = reduce_left(kSub * R, S::CL);
-                    constexpr int kSame = S::CL > kSub * R ? S::CL / (kSub * R) : 1;
-                    if ((lane / L) % kSame == 0) {
+                    const int f0 = reduce_lanes<kSub * R, CL, L>(f, lane);
+                    constexpr int kVals = reduce_left(kSub * R, CL);
+                    constexpr int kCopies = CL > kSub * R ? CL / (kSub * R) : 1;
+                    if ((lane / L) % kCopies == 0) {
 #pragma unroll
-                        for (int i = 0; i < kLeft; ++i) {
-                            const int k = (first + i) / R, r = (first + i) % R;
+                        for (int i = 0; i < kVals; ++i) {
+                            const int k = (f0 + i) / R, r = (f0 + i) % R;
                             part[((w * kWarps + warp) * kSub + k) * NP + j * R + r] = f[i];
                         }
                     }
                 }
                 __syncthreads();
+                float *oB = b.part_B + (((long)gtile * T + t0 + sub * kSub) * a.ngroups + grp) * N;
+                float *oC = b.part_C + (((long)gtile * T + t0 + sub * kSub) * a.ngroups + grp) * N;
                 for (int e = tid; e < 2 * kSub * NP; e += kBwdThreads) {
                     const int w = e / (kSub * NP), k = (e / NP) % kSub, n = e % NP;
                     float sum = 0.f;
 #pragma unroll
                     for (int i = 0; i < kWarps; ++i) sum += part[((w * kWarps + i) * kSub + k) * NP + n];
-                    const int t = sub * kSub + k;
-                    if (t < n_tok && n < N)
-                        (w ? b.part_C : b.part_B)[(((long)gtile * T + t0 + t) * a.ngroups + grp) * N + n] = sum;
+                    if (sub * kSub + k < n_tok && n < N) (w ? oC : oB)[k * a.ngroups * N + n] = sum;
                 }
             }
-            __syncthreads();
-            // per (token, channel) outputs, from the sums over n and the inputs again
-            for (int k0 = st; k0 < n_tok && slive; k0 += RS * kStep) {
-                uint32_t rv[kStep], rx[kStep], rg[kStep], rz[kStep];
-#pragma unroll
-                for (int i = 0; i < kStep; ++i) {
-                    const long t = t0 + min(k0 + i * RS, n_tok - 1);
-                    rv[i] = raw_load<TDt>(a.dt, t * a.dt_stride + ds);
-                    rx[i] = raw_load<TIn>(a.x, t * a.x_stride + ds);
-                    rg[i] = raw_load<TIn>(b.dy, t * b.dy_stride + ds);
-                    rz[i] = a.z ? raw_load<TIn>(a.z, t * a.z_stride + ds) : 0u;
-                }
-#pragma unroll
-                for (int i = 0; i < kStep; ++i) {
-                    const int k = k0 + i * RS;
-                    if (k >= n_tok) break;
-                    const long t = t0 + k;
-                    const float raw = raw_value<TDt>(rv[i]), x = raw_value<TIn>(rx[i]);
-                    const float v = dt_value(a.dtp, raw, bias), w = s_u[k * CB + sc];
-                    float dy = raw_value<TIn>(rg[i]);
-                    if (a.z) {
-                        const float z = raw_value<TIn>(rz[i]);
-                        const float sg = rcp_approx(1.f + ex2_approx(-z * kLog2e));
-                        store_out(static_cast<TIn *>(b.dz) + t * a.dim + ds,
-                                  dy * fmaf(skip, x, s_g[k * CB + sc]) * sg * fmaf(z, 1.f - sg, 1.f));
-                        dy *= z * sg;
-                    }
-                    const float ddt = fmaf(s_v[k * CB + sc], kLn2, w * x) * dt_slope(a.dtp, raw, bias);
-                    store_out(static_cast<TIn *>(b.dx) + t * a.dim + ds, fmaf(w, v, skip * dy));
-                    store_out(static_cast<TDt *>(b.ddt) + t * a.dim + ds, ddt);
-                    sum_D = fmaf(dy, x, sum_D);
-                    sum_bias += ddt;
-                }
-            }
-            __syncthreads();
+            // the last sub-tile's barrier lies behind every read of the staged chunk: the next may be staged
         }
         if (b.dinitial) {
 #pragma unroll
             for (int q = 0; q < CS; ++q) {
-                const int d = c0 + ch0 + q * S::CL;
+                const int d = c0 + ch0 + q * CL;
                 if (d < cend) store_row<R>(b.dinitial + ((long)s * a.dim + d) * N, j, N, G[q]);
             }
         }
@@ -350,19 +381,18 @@ selective_scan_bwd_kernel(SelScanBwdArgs b, int units)
 
 #pragma unroll
     for (int q = 0; q < CS; ++q) {
-        const int d = c0 + ch0 + q * S::CL;
-        if (d < cend) store_row<R>(b.part_A + ((long)unit * a.dim + d) * N, j, N, dA[q]);
-    }
-    s_v[tid] = sum_D;
-    s_u[tid] = sum_bias;
-    __syncthreads();
-    if (st == 0 && slive) {
-        for (int i = 1; i < RS; ++i) {
-            sum_D += s_v[i * CB + sc];
-            sum_bias += s_u[i * CB + sc];
+        const int d = c0 + ch0 + q * CL;
+#pragma unroll
+        for (int o = L / 2; o > 0; o >>= 1) {
+            sum_D[q] += __shfl_xor_sync(0xffffffffu, sum_D[q], o);
+            sum_bias[q] += __shfl_xor_sync(0xffffffffu, sum_bias[q], o);
         }
-        b.part_D[(long)unit * a.dim + ds] = sum_D;
-        b.part_bias[(long)unit * a.dim + ds] = sum_bias;
+        if (d >= cend) continue;
+        store_row<R>(b.part_A + ((long)unit * a.dim + d) * N, j, N, dA[q]);
+        if (j == 0) {
+            b.part_D[(long)unit * a.dim + d] = sum_D[q];
+            b.part_bias[(long)unit * a.dim + d] = sum_bias[q];
+        }
     }
 }
 

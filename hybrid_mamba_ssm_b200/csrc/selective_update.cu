@@ -21,7 +21,7 @@ constexpr int kUpThreads = 256;
 constexpr int kRows = 4;
 
 template <typename TIn, typename TDt, int L, bool kVec>
-__global__ void __launch_bounds__(kUpThreads)
+__global__ void __launch_bounds__(kUpThreads, 4)
 selective_update_kernel(SelUpdateArgs a, int ctiles)
 {
     constexpr int CT = kUpThreads / L;
