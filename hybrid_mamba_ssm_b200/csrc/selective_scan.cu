@@ -243,7 +243,7 @@ selective_scan_kernel(SelScanArgs a)
             const int o = y0 + i * RS * a.dim;
             if (a.y_bf16) {
                 __nv_bfloat16 *yp = static_cast<__nv_bfloat16 *>(a.y) + yt + o;
-                if (slive1 && a.dim % 2 == 0) {
+                if (slive1 && gdim % 2 == 0) {      // the even channel of a pair is even in y too
                     *reinterpret_cast<__nv_bfloat162 *>(yp) = __floats2bfloat162_rn(lo2(y), hi2(y));
                 } else {
                     store_out(yp, lo2(y));

@@ -660,6 +660,8 @@ def _token_rows(t, name, lead, row, dev, dtype):
         raise ValueError(f"{name} must have shape {lead + row}, got {tuple(shape)}")
     k = len(lead)
     width = row[0] if len(row) == 1 else row[0] * row[1]
+    if 0 in lead:
+        return width
     if (row[-1] > 1 and strides[-1] != 1) or (len(row) == 2 and row[0] > 1 and strides[k] != row[1]):
         raise ValueError(f"the rows of {name} must be contiguous")
     if k == 1:
