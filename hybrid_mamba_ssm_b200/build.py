@@ -1,7 +1,9 @@
-"""Build libssm.so (the CUDA library behind include/ssm.h) in-tree with nvcc.
+"""Build libssm.so (the CUDA library behind include/ssm.h) in-tree with nvcc,
+and the Python binding's _marshal module with the C++ compiler.
 
 Every .cu file under csrc/ is compiled for sm_100a and linked into
-hybrid_mamba_ssm_b200/libssm.so.  Run ``python -m hybrid_mamba_ssm_b200.build``
+hybrid_mamba_ssm_b200/libssm.so; csrc/marshal.cpp becomes
+hybrid_mamba_ssm_b200/_marshal.so, linked against it and torch.  Run ``python -m hybrid_mamba_ssm_b200.build``
 or call ``build()``.
 """
 from __future__ import annotations
@@ -11,12 +13,14 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libssm.so")
+MARSHAL = os.path.join(HERE, "_marshal.so")
 BUILD_DIR = os.path.join(ROOT, "_build")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
@@ -66,7 +70,31 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
             print(" ".join(cmd), flush=True)
         subprocess.check_call(cmd)
         os.replace(tmp, LIB)
+    build_marshal(force, verbose)
     return LIB
+
+
+def build_marshal(force: bool = False, verbose: bool = False) -> str:
+    """Compile csrc/marshal.cpp into _marshal.so (host code only)."""
+    src = os.path.join(CSRC, "marshal.cpp")
+    if not force and not _stale(MARSHAL, [src, os.path.join(ROOT, "include", "ssm.h")]):
+        return MARSHAL
+    import torch
+    troot = os.path.dirname(torch.__file__)
+    cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(_nvcc()))), "include")
+    tmp = MARSHAL + f".tmp{os.getpid()}"
+    cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-I" + os.path.join(ROOT, "include"), "-isystem", sysconfig.get_paths()["include"],
+           "-isystem", os.path.join(troot, "include"),
+           "-isystem", os.path.join(troot, "include", "torch", "csrc", "api", "include"), "-isystem", cuda,
+           src, "-o", tmp, "-L" + HERE, "-l:libssm.so", "-L" + os.path.join(troot, "lib"), "-ltorch_python",
+           "-ltorch_cpu", "-lc10_cuda", "-lc10", "-Wl,-rpath,$ORIGIN"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    subprocess.check_call(cmd)
+    os.replace(tmp, MARSHAL)
+    return MARSHAL
 
 
 if __name__ == "__main__":

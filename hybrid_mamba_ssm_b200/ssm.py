@@ -113,6 +113,11 @@ def _load():
 
 
 lib = _load()
+try:
+    from . import _marshal
+except ImportError as e:
+    raise ImportError("_marshal.so is not built or does not load; run "
+                      "`python -m hybrid_mamba_ssm_b200.build`") from e
 
 
 class DtParams(ctypes.Structure):
@@ -605,7 +610,20 @@ def ssm_gated_rmsnorm(y, z, weight, group_size: int, eps: float = 1e-5, out=None
 # ---------------------------------------------------------------------------
 # Per-channel selective scan, its gradient and decode update, the conv1d
 # gradient, and the rows of state pools.
+#
+# Each call first goes to its function of the _marshal module, which does the
+# same checks and allocations in C++ for a call that is plainly right (tensors
+# of the current device, default stream and workspace).  It answers None for
+# anything else; the Python below then names what is wrong, or takes the
+# options that _marshal does not.
 # ---------------------------------------------------------------------------
+def _plain(answer, where):
+    """Whether _marshal made the call (its results are `answer`); raises on a library error."""
+    if answer.__class__ is int:
+        raise SSMError(answer, where)
+    return answer is not None
+
+
 @contextlib.contextmanager
 def _enter(device, stream):
     with torch.cuda.device(device), torch.cuda.stream(stream):
@@ -747,6 +765,11 @@ def selective_scan_fwd(x, dt, A, B, C, D=None, z=None, initial_state=None, cu_se
         run in concurrent ranges.
     Returns (y, final_state), or (y, final_state, saved) with save_states.
     """
+    if stream is None and workspace == "auto" and y_dtype is None:
+        out = _marshal.scan_fwd(x, cu_seqlens, dt, A, B, C, D, z, dt_bias, dt_softplus, dt_limit, initial_state,
+                                final_state, slot_idx, has_initial_state, y, return_final_state, save_states, status)
+        if _plain(out, "selective_scan_fwd"):
+            return out if save_states else out[:2]
     with _scope(x, stream):
         dev = x.get_device()
         lead, nseq, seqlen, T, dim = _scan_lead(x, cu_seqlens, dev)
@@ -811,6 +834,11 @@ def selective_scan_bwd(dy, x, dt, A, B, C, saved, D=None, z=None, dfinal_state=N
     save_states=True (`saved` is its third result).  dy : like x.
     dfinal_state : [nseq, dim, d_state] fp32 or None.  The gradients have their
     inputs' shapes and types (contiguous)."""
+    if stream is None and workspace == "auto":
+        out = _marshal.scan_bwd(x, cu_seqlens, dt, A, B, C, D, z, dt_bias, dt_softplus, dt_limit, dy, saved,
+                                dfinal_state, want_dinitial, status)
+        if _plain(out, "selective_scan_bwd"):
+            return SelectiveScanGrads(*out)
     with _scope(x, stream):
         dev = x.get_device()
         lead, nseq, seqlen, T, dim = _scan_lead(x, cu_seqlens, dev)
@@ -853,6 +881,10 @@ def selective_state_update(state, x, dt, A, B, C, D=None, z=None, slot_idx=None,
     x, dt, z : [batch, dim];  B, C : [batch, G, d_state];  A, D, dt_bias and the
     dt transform as for selective_scan_fwd.  Returns y [batch, dim] (padding
     rows left as they were)."""
+    if stream is None and y_dtype is None:
+        out = _marshal.state_update(x, dt, A, B, C, D, z, dt_bias, dt_softplus, dt_limit, state, slot_idx, y, status)
+        if _plain(out, "selective_state_update"):
+            return out[0]
     with _scope(x, stream):
         if x.dim() != 2:
             raise ValueError("x must be [batch, dim]")
@@ -879,6 +911,11 @@ def causal_conv1d_bwd(dy, x, weight, bias=None, initial_state=None, dfinal_state
     its conv_state), or None; dfinal_state : gradient of the states it left, or
     None.  Returns (dx, dweight, dbias, dinitial_state); dbias is None without
     bias, dinitial_state None without initial_state."""
+    if stream is None and workspace == "auto":
+        out = _marshal.conv1d_bwd(x, cu_seqlens, dy, weight, bias, initial_state, dfinal_state,
+                                  _activation(activation), status)
+        if _plain(out, "causal_conv1d_bwd"):
+            return out
     with _scope(x, stream):
         dev = x.get_device()
         in_code = _dtype_code(x.dtype)
@@ -936,6 +973,8 @@ def ssm_pool_copy(pools, src_idx, dst_idx, status=None, stream=None) -> None:
     one row to several).  pools : one tensor or a list of tensors [max_slots,
     ...] with contiguous rows (any types); src_idx, dst_idx : int32 [n], an
     entry with a negative index is skipped."""
+    if stream is None and _plain(_marshal.pool_copy(pools, src_idx, dst_idx, status), "ssm_pool_copy"):
+        return
     arr, n, slots, like = _pools(pools)
     with _scope(like, stream):
         dev, pairs = like.get_device(), src_idx.shape[0]
@@ -947,6 +986,8 @@ def ssm_pool_copy(pools, src_idx, dst_idx, status=None, stream=None) -> None:
 
 def ssm_pool_zero(pools, row_idx, status=None, stream=None) -> None:
     """Rows row_idx (int32 [n]; negative: skipped) of every pool <- 0."""
+    if stream is None and _plain(_marshal.pool_zero(pools, row_idx, status), "ssm_pool_zero"):
+        return
     arr, n, slots, like = _pools(pools)
     with _scope(like, stream):
         dev, rows = like.get_device(), row_idx.shape[0]
@@ -959,6 +1000,10 @@ def ssm_pool_compact(pools, slot_idx, status=None, stream=None, workspace="auto"
     """Moves the live rows (those that slot_idx, int32 [nrows], names) to the
     front of every pool and rewrites slot_idx in place.  Returns their number,
     an int32 scalar tensor."""
+    if stream is None and workspace == "auto":
+        out = _marshal.pool_compact(pools, slot_idx, status)
+        if _plain(out, "ssm_pool_compact"):
+            return out[0]
     arr, n, slots, like = _pools(pools)
     with _scope(like, stream):
         dev, rows = like.get_device(), slot_idx.shape[0]
