@@ -81,8 +81,9 @@ size_t selective_scan_workspace_size(int nseq, long long ntokens, int dim, int d
     if (nseq <= 0 || ntokens <= 0 || dim <= 0 || d_state <= 0 || d_state > 256 || ngroups <= 0 || dim % ngroups)
         return 0;
     int span;
-    const int ranges = ssm::selective_scan_ranges(nseq, ntokens, dim, d_state, ngroups, &span);
-    return ranges ? 2 * up16((size_t)ranges * dim * d_state * sizeof(float)) + (size_t)ranges * dim * sizeof(float) : 0;
+    const int units = ssm::selective_scan_segments(nseq, ntokens, dim, d_state, ngroups, &span);
+    const size_t row = (size_t)dim * d_state * sizeof(float);
+    return units ? up16(units * row) + up16(nseq * row) + (size_t)units * dim * sizeof(float) : 0;
 }
 
 int selective_scan_fwd(int nseq, int seqlen, const int32_t *cu_seqlens, int dim, int d_state, int ngroups,
@@ -118,7 +119,7 @@ int selective_scan_fwd(int nseq, int seqlen, const int32_t *cu_seqlens, int dim,
 
     const long long srow = (long long)dim * d_state, nrows = slot_idx ? max_slots : nseq;
     const size_t need = selective_scan_workspace_size(nseq, T, dim, d_state, ngroups);
-    const bool cut = need && workspace && workspace_bytes >= need && !saved_states;
+    const bool cut = need && workspace && workspace_bytes >= need;
     const Range outs[] = {range_of(y, (size_t)T * dim * dtype_size(y_dtype)), f32_range(final_state, nrows * srow),
                           range_of(saved_states, saved_states ? selective_scan_saved_size(nseq, T, dim, d_state) : 0),
                           range_of(workspace, workspace ? workspace_bytes : 0)};
@@ -144,13 +145,14 @@ int selective_scan_fwd(int nseq, int seqlen, const int32_t *cu_seqlens, int dim,
     a.slot_idx = slot_idx; a.has_initial = has_initial_state; a.max_slots = max_slots;
     a.y = y; a.saved = saved_states; a.status_dev = status_dev;
     a.pairs = dim / ngroups % 2 == 0 && paired(rows[0]) && paired(rows[1]) && paired(rows[4]);
+    a.units = nseq;
     if (cut) {
-        a.ranges = ssm::selective_scan_ranges(nseq, T, dim, d_state, ngroups, &a.span);
-        const size_t n = up16((size_t)a.ranges * srow * sizeof(float));
+        a.units = ssm::selective_scan_segments(nseq, T, dim, d_state, ngroups, &a.span);
+        const size_t n = up16((size_t)a.units * srow * sizeof(float));
         char *w = static_cast<char *>(workspace);
         a.range_state = reinterpret_cast<float *>(w);
         a.range_initial = reinterpret_cast<float *>(w + n);
-        a.range_dt = reinterpret_cast<float *>(w + 2 * n);
+        a.range_dt = reinterpret_cast<float *>(w + n + up16((size_t)nseq * srow * sizeof(float)));
     }
     return ssm::launch_selective_scan(a, stream) == cudaSuccess ? SSM_OK : SSM_ERR_CUDA;
 }

@@ -253,7 +253,8 @@ PyObject *scan_fwd(PyObject *, PyObject *const *p, Py_ssize_t n) {
         size_t wsb = 0;
         if (save) {
             saved = fresh(x, {(int64_t)(selective_scan_saved_size((int)t.nseq, t.T, (int)t.dim, (int)o.N) / 4)}, at::kFloat);
-        } else if ((wsb = selective_scan_workspace_size((int)t.nseq, t.T, (int)t.dim, (int)o.N, (int)o.G))) {
+        }
+        if ((wsb = selective_scan_workspace_size((int)t.nseq, t.T, (int)t.dim, (int)o.N, (int)o.G))) {
             ws = fresh(x, {(int64_t)wsb}, at::kByte);
         }
         const int st = selective_scan_fwd(

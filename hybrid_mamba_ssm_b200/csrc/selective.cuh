@@ -168,6 +168,16 @@ __device__ __forceinline__ f32x2 dt_value2(const DtParams &p, f32x2 raw, f32x2 b
         v = pack2(fminf(fmaxf(lo2(v), p.lo), p.hi), fminf(fmaxf(hi2(v), p.lo), p.hi));
     return v;
 }
+__device__ __forceinline__ f32x2 dt_slope2(const DtParams &p, f32x2 raw, f32x2 bias) {
+    if (p.clamp)   // rare: one by one
+        return pack2(dt_slope(p, lo2(raw), lo2(bias)), dt_slope(p, hi2(raw), hi2(bias)));
+    if (!p.softplus) return pack2(1.f, 1.f);
+    const f32x2 v = add2(raw, bias);
+    const f32x2 a = pack2(min_nan(fabsf(lo2(v)), 120.f), min_nan(fabsf(hi2(v)), 120.f));
+    const f32x2 e = ex2_pair(mul2(a, pack2(-kLog2e, -kLog2e))), d = add2(e, pack2(1.f, 1.f));
+    const float r0 = rcp_approx(lo2(d)), r1 = rcp_approx(hi2(d));
+    return pack2(lo2(v) >= 0.f ? r0 : lo2(e) * r0, hi2(v) >= 0.f ? r1 : hi2(e) * r1);
+}
 __device__ __forceinline__ f32x2 silu2(f32x2 z) {
     const f32x2 d = add2(ex2_pair(mul2(z, pack2(-kLog2e, -kLog2e))), pack2(1.f, 1.f));
     return mul2(z, pack2(rcp_approx(lo2(d)), rcp_approx(hi2(d))));
@@ -184,6 +194,10 @@ template <typename T>
 __device__ __forceinline__ float raw_value(uint32_t r) {
     return __uint_as_float(sizeof(T) == 2 ? r << 16 : r);
 }
+__device__ __forceinline__ void prefetch_l2(const void *p) {
+    asm volatile("prefetch.global.L2 [%0];" :: "l"(p));
+}
+
 // Two adjacent values.  pair_load wants an address aligned to both; either way
 // the registers hold what pair_value takes: a bf16 pair is one register, or
 // two with a value in the low half of each.
@@ -196,6 +210,17 @@ __device__ __forceinline__ void pair_load(const T *p, int i, uint32_t (&r)[2]) {
         const uint2 q = *reinterpret_cast<const uint2 *>(p + i);
         r[0] = q.x;
         r[1] = q.y;
+    }
+}
+// Stores v[0], and v[1] when `both`: as one aligned access when `aligned`.
+template <typename T>
+__device__ __forceinline__ void store_pair(T *p, f32x2 v, bool aligned, bool both) {
+    if (aligned) {
+        if constexpr (sizeof(T) == 2) *reinterpret_cast<__nv_bfloat162 *>(p) = __floats2bfloat162_rn(lo2(v), hi2(v));
+        else *reinterpret_cast<float2 *>(p) = make_float2(lo2(v), hi2(v));
+    } else {
+        store_out(p, lo2(v));
+        if (both) store_out(p + 1, hi2(v));
     }
 }
 template <typename T>
@@ -229,5 +254,68 @@ __device__ __forceinline__ bool seq_range(const SelScanArgs &a, long T, int s, l
     hi = a.cu_seqlens[s + 1];
     return lo >= 0 && hi >= lo && hi <= T && (s > 0 || lo == 0) && (s < a.nseq - 1 || hi == T);
 }
+
+// Units of work: a sequence, or a segment of `span` tokens of one (span: a
+// multiple of kSavedEvery; 0: whole sequences).  Segment k of sequence s is
+// unit start(s) / span + s + k of start(end) / span + nseq: sequences never
+// share a unit (see saved_row), and some units have no tokens.
+struct Unit {
+    int s, k;
+    long lo, hi;   // the sequence
+    long b, e;     // the unit's tokens
+    long base;     // the sequence's segment 0
+};
+__device__ __forceinline__ bool find_unit(const SelScanArgs &a, long T, int u, Unit &q) {
+    auto base = [&](int s) { return (a.cu_seqlens ? (long)a.cu_seqlens[s] : (long)s * a.seqlen) / a.span + s; };
+    q.s = u;
+    q.k = 0;
+    q.base = u;
+    if (a.span) {
+        int lo = 0, hi = a.nseq - 1;
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (base(mid) <= u) lo = mid; else hi = mid - 1;
+        }
+        q.s = lo;
+        q.base = base(lo);
+        if (q.base > u) return false;
+        q.k = (int)(u - q.base);
+    }
+    if (!seq_range(a, T, q.s, q.lo, q.hi)) {
+        report_status(a.status_dev, kStatusDeviceInput);
+        return false;
+    }
+    q.b = a.span ? q.lo + (long)q.k * a.span : q.lo;
+    q.e = a.span ? min(q.b + a.span, q.hi) : q.hi;
+    return q.k == 0 || q.b < q.hi;
+}
+
+// With segments, a unit is found by searching the offsets, which inconsistent
+// ones can lead past a sequence: one CTA looks at them all, to report them.
+__device__ __forceinline__ void check_offsets(const SelScanArgs &a, long T) {
+    if (!a.span || blockIdx.x || !a.cu_seqlens) return;
+    long lo, hi;
+    for (int s = threadIdx.x; s < a.nseq; s += blockDim.x)
+        if (!seq_range(a, T, s, lo, hi)) report_status(a.status_dev, kStatusDeviceInput);
+}
+
+// The sequence with the u-th longest range (ties by index): packed batches run
+// longest first, so that the last CTAs to start are short.  Every thread of
+// the CTA takes part; nseq is at most blockDim.x.
+__device__ __forceinline__ int longest_first(const SelScanArgs &a, int u, int *shared) {
+    const int i = threadIdx.x;
+    if (i < a.nseq) {
+        const int len = a.cu_seqlens[i + 1] - a.cu_seqlens[i];
+        int rank = 0;
+        for (int k = 0; k < a.nseq; ++k) {
+            const int other = a.cu_seqlens[k + 1] - a.cu_seqlens[k];
+            rank += other > len || (other == len && k < i);
+        }
+        if (rank == u) *shared = i;
+    }
+    __syncthreads();
+    return *shared;
+}
+constexpr int kMaxRanked = 64;
 
 }  // namespace ssm

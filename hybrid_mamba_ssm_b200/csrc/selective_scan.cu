@@ -85,28 +85,16 @@ __device__ __forceinline__ void store_states(float *row, int j, int N, const f32
     }
 }
 
-// Sequence that holds token t (t < T): the last s with start <= t.
-__device__ __forceinline__ int seq_of(const SelScanArgs &a, long t) {
-    if (!a.cu_seqlens) return (int)(t / a.seqlen);
-    int lo = 0, hi = a.nseq - 1;
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (a.cu_seqlens[mid] <= t) lo = mid; else hi = mid - 1;
-    }
-    return lo;
-}
-
 enum { kWhole = 0, kRangeState = 1, kRangeOut = 2 };
 
 // kWhole: one CTA per (sequence, channel tile).
-// kRangeState / kRangeOut: one CTA per (range of the token stream, channel
-// tile), two launches.  The first leaves, for every range whose last sequence
-// goes on behind it, the state that the range's own tokens build from zero (or
-// from the sequence's initial state, where it starts inside the range) and the
-// sum of its step sizes: the range multiplies the state that enters it by
-// exp(A sum v).  It also copies the initial state of a sequence that goes on
-// behind the range.  The second folds the ranges before its own and runs its
-// tokens from the state that enters.
+// kRangeState / kRangeOut: one CTA per (segment of a sequence, channel tile),
+// two launches.  The first leaves, for every segment but a sequence's last, the
+// state that its own tokens build from zero (the first one: from the initial
+// state) and the sum of its step sizes: the segment multiplies the state that
+// enters it by exp(A sum v).  It also copies the initial state.  The second
+// folds the segments before its own and runs its tokens from the state that
+// enters.
 template <typename TIn, typename TDt, int R, int L, int Q, int kMode>
 __global__ void __launch_bounds__(kThreads, kMinBlocks<R, Q>)
 selective_scan_kernel(SelScanArgs a)
@@ -358,70 +346,48 @@ selective_scan_kernel(SelScanArgs a)
         for (int q = 0; q < Q; ++q)
             if (live(q)) store_states<R>(const_cast<float *>(row_of(rows, row, q)), j, N, h[q]);
     };
-    auto one_sequence = [&](int s, long r0, long r1) {   // its tokens within [r0, r1)
-        long lo, hi;
-        if (!seq_range(a, T, s, lo, hi)) {
-            report_status(a.status_dev, kStatusDeviceInput);
-            return;
-        }
-        if (lo < r0 && hi <= r0) return;                  // ended in an earlier range
-        bool init;
-        const long row = state_row(s, init);
-        if (row < 0) return;
-        if (kMode == kRangeOut && lo < r0) {
-            // the state entering this range: the ranges since the sequence's start, folded
-            const int first = (int)(lo / a.span), own = (int)(r0 / a.span);
-            load_all(a.range_state, first, h);
-            for (int i = first + 1; i < own; ++i) {
-                f32x2 e[Q][P];
-                load_all(a.range_state, i, e);
-#pragma unroll
-                for (int q = 0; q < Q; ++q) {
-                    const float v = live(q) ? a.range_dt[(long)i * a.dim + d0 + q * CS] : 0.f;
-#pragma unroll
-                    for (int p = 0; p < P; ++p)
-                        h[q][p] = fma2(ex2_pair(mul2(pack2(v, v), A[q][p])), h[q][p], e[q][p]);
-                }
-            }
-        } else if (kMode == kRangeOut && hi > r1) {
-            // its row may be written (in place) by the range it ends in: the copy is read
-            load_all(a.range_initial, r0 / a.span, h);
-        } else {
-            load_all(init ? a.initial : nullptr, row, h);
-        }
-        const long b = max(lo, r0), e = min(hi, r1);
-        if (b < e) run(b, e, lo, lo / kSavedEvery + s);
-        if (hi <= r1 && a.final && (lo < hi || a.final != a.initial || !init)) store_all(a.final, row);
-    };
-
-    if (kMode == kWhole) {
-        one_sequence(unit, 0, T);
-    } else if (kMode == kRangeState) {
-        const long r0 = (long)unit * a.span, r1 = r0 + a.span;   // never the last range: r1 < T
-        const int s = seq_of(a, r1 - 1);
-        long lo, hi;
-        bool init;
-        if (!seq_range(a, T, s, lo, hi) || lo >= r1 || hi <= r1) return;
-        const long row = state_row(s, init);
-        if (row < 0) return;
-        load_all(init && lo >= r0 ? a.initial : nullptr, row, h);
-        if (lo >= r0) store_all(a.range_initial, unit);
-        run(max(lo, r0), r1, lo, 0);
+    __shared__ int s_seq;
+    Unit w;
+    if (!find_unit(a, T, kMode == kWhole && a.cu_seqlens && a.nseq > 1 && a.nseq <= kMaxRanked ? longest_first(a, unit, &s_seq) : unit, w)) {
+        check_offsets(a, T);
+        return;
+    }
+    check_offsets(a, T);
+    bool init;
+    const long row = state_row(w.s, init);
+    if (row < 0) return;
+    if (kMode == kRangeState) {
+        if (w.e == w.hi) return;                           // the last segment: nothing follows it
+        load_all(init && w.k == 0 ? a.initial : nullptr, row, h);
+        if (w.k == 0) store_all(a.range_initial, w.s);
+        run(w.b, w.e, w.lo, 0);
         store_all(a.range_state, unit);
 #pragma unroll
         for (int q = 0; q < Q; ++q)
             if (j == 0 && live(q)) a.range_dt[(long)unit * a.dim + d0 + q * CS] = vsum[q];
-    } else {
-        const long r0 = (long)unit * a.span, r1 = min(r0 + a.span, T);
-        int s = seq_of(a, r0);
-        // empty sequences that lie at r0, before the one that holds it
-        while (a.cu_seqlens && s > 0 && a.cu_seqlens[s - 1] >= r0) --s;
-        for (; s < a.nseq; ++s) {
-            const long lo = a.cu_seqlens ? (long)a.cu_seqlens[s] : (long)s * a.seqlen;
-            if (lo >= r1 && r1 < T) break;
-            one_sequence(s, r0, r1);
-        }
+        return;
     }
+    if (kMode == kRangeOut && w.k > 0) {
+        load_all(a.range_state, w.base, h);
+        for (int i = 1; i < w.k; ++i) {
+            f32x2 e[Q][P];
+            load_all(a.range_state, w.base + i, e);
+#pragma unroll
+            for (int q = 0; q < Q; ++q) {
+                const float v = live(q) ? a.range_dt[(w.base + i) * a.dim + d0 + q * CS] : 0.f;
+#pragma unroll
+                for (int p = 0; p < P; ++p)
+                    h[q][p] = fma2(ex2_pair(mul2(pack2(v, v), A[q][p])), h[q][p], e[q][p]);
+            }
+        }
+    } else if (kMode == kRangeOut && w.e < w.hi) {
+        // its row may be written (in place) by the segment it ends in: the copy is read
+        load_all(a.range_initial, w.s, h);
+    } else {
+        load_all(init ? a.initial : nullptr, row, h);
+    }
+    if (w.b < w.e) run(w.b, w.e, w.lo, w.lo / kSavedEvery + w.s);
+    if (w.e == w.hi && a.final && (w.lo < w.hi || a.final != a.initial || !init)) store_all(a.final, row);
 }
 
 template <typename TIn, typename TDt, int R, int L, int Q>
@@ -429,14 +395,14 @@ cudaError_t launch_shape(const SelScanArgs &a, cudaStream_t stream)
 {
     const int gdim = a.dim / a.ngroups, CT = ScanShape<R, L, Q>::CT;
     const long long tiles = (long long)((gdim + CT - 1) / CT) * a.ngroups;
-    if (tiles * (a.ranges ? a.ranges : a.nseq) > 0x7fffffffLL) return cudaErrorInvalidValue;
-    if (!a.ranges) {
-        selective_scan_kernel<TIn, TDt, R, L, Q, kWhole><<<(unsigned)(tiles * a.nseq), kThreads, 0, stream>>>(a);
+    if (tiles * a.units > 0x7fffffffLL) return cudaErrorInvalidValue;
+    const unsigned blocks = (unsigned)(tiles * a.units);
+    if (!a.span) {
+        selective_scan_kernel<TIn, TDt, R, L, Q, kWhole><<<blocks, kThreads, 0, stream>>>(a);
         return cudaGetLastError();
     }
-    if (a.ranges > 1)
-        selective_scan_kernel<TIn, TDt, R, L, Q, kRangeState><<<(unsigned)(tiles * (a.ranges - 1)), kThreads, 0, stream>>>(a);
-    selective_scan_kernel<TIn, TDt, R, L, Q, kRangeOut><<<(unsigned)(tiles * a.ranges), kThreads, 0, stream>>>(a);
+    selective_scan_kernel<TIn, TDt, R, L, Q, kRangeState><<<blocks, kThreads, 0, stream>>>(a);
+    selective_scan_kernel<TIn, TDt, R, L, Q, kRangeOut><<<blocks, kThreads, 0, stream>>>(a);
     return cudaGetLastError();
 }
 
@@ -459,11 +425,13 @@ cudaError_t launch_types(const SelScanArgs &a, cudaStream_t stream)
 static int lanes_for(int N) { return N <= 4 ? 1 : N <= 8 ? 2 : N <= 16 ? 4 : N <= 32 ? 8 : N <= 64 ? 16 : 32; }
 
 // A sequence is a chain of its tokens: nseq * dim channels give
-// nseq * dim * lanes / 32 warps, however long it is.  Cutting the stream costs
-// the ranges' first pass (about 0.6 of the work again), so it is done where
-// the chains fill less than a third of the warps that the device holds, into
-// as many ranges as fill it, of at least 128 tokens.
-int selective_scan_ranges(int nseq, long T, int dim, int d_state, int ngroups, int *span)
+// nseq * dim * lanes / 32 warps, however long it is.  Cutting sequences costs
+// the first pass over the segments (about 0.6 of the work again), so it is
+// done where the chains fill less than a third of the warps that the device
+// holds, into segments of at least 128 tokens, as many as fill it.  (1 x 32768
+// tokens, 2048 channels of 16 states: 2.8 ms as one chain, 0.9 ms cut.)
+// Returns the number of units, 0 for whole sequences.
+int selective_scan_segments(int nseq, long T, int dim, int d_state, int ngroups, int *span)
 {
     *span = 0;
     int dev = 0, sms = 0;
@@ -474,13 +442,13 @@ int selective_scan_ranges(int nseq, long T, int dim, int d_state, int ngroups, i
     }
     const double warps = (double)dim * lanes_for(d_state) / 32, room = 28.0 * sms;
     if (warps * nseq * 3 > room) return 0;
-    long ranges = (long)(room / warps);
-    if (ranges > T / 128) ranges = T / 128;
-    if (ranges > 256) ranges = 256;
-    if (ranges < 3 || ranges <= 2L * nseq) return 0;
-    const long n = (T + ranges - 1) / ranges, len = (n + kSavedEvery - 1) / kSavedEvery * kSavedEvery;
-    *span = (int)len;
-    return (int)((T + len - 1) / len);
+    long segments = (long)(room / warps);
+    if (segments > T / 128) segments = T / 128;
+    if (segments > 256) segments = 256;
+    if (segments < 3 || segments <= 2L * nseq) return 0;
+    const long n = (T + segments - 1) / segments;
+    *span = (int)((n + kSavedEvery - 1) / kSavedEvery * kSavedEvery);
+    return (int)(T / *span + nseq);
 }
 
 cudaError_t launch_selective_scan(const SelScanArgs &a, cudaStream_t stream)

@@ -38,7 +38,7 @@ constexpr int kSub = 4;                          // tokens of a sub-tile
 constexpr int kSubs = kSavedEvery / kSub;        // sub-tiles of a chunk
 constexpr int kWarps = 4;
 constexpr int kBwdThreads = 32 * kWarps;
-constexpr int kMaxUnits = 64;                    // sequences are dealt to at most this many CTAs per tile
+constexpr int kMaxCtas = 64;                     // whole sequences are dealt to at most this many CTAs per tile
 
 template <int R, int L, int CS>
 struct BwdShape {
@@ -46,11 +46,15 @@ struct BwdShape {
     static constexpr int CW = CL * CS;           // channels of a warp
     static constexpr int CB = CW * kWarps;       // channels of a CTA
     static constexpr int NP = R * L;
-    // floats of shared memory: v and v x, gated dy; B, C; sub-tile states; parts of dB, dC (two buffers)
+    // floats of shared memory: v and v x, gated dy; B, C; states in front of all
+    // sub-tiles but the last (which is still in registers); every thread's dB, dC
+    // of a sub-tile, 4 floats apart more so that eight 16-byte accesses of a warp
+    // fall into different banks
     static constexpr int kRow = kSavedEvery * CB;
-    static constexpr int kStates = kSubs * CS * kBwdThreads * R;
-    static constexpr int kParts = 2 * 2 * kWarps * kSub * NP;
-    static constexpr size_t kBytes = sizeof(float) * (3 * kRow + 2 * kSavedEvery * NP + kStates + kParts);
+    static constexpr int kStates = (kSubs - 1) * CS * kBwdThreads * R;
+    static constexpr int kVals = 2 * kSub * R, kPitch = kVals + 4;
+    static constexpr size_t kStaged = sizeof(float) * (3 * kRow + 2 * kSavedEvery * NP);
+    static constexpr size_t kBytes = kStaged + sizeof(float) * (kStates + kBwdThreads * kPitch);
     static_assert(CB % 2 == 0 && kBwdThreads % (CB / 2) == 0, "a staging thread keeps its two channels");
 };
 
@@ -95,9 +99,19 @@ __device__ __forceinline__ void store_row(float *row, int j, int N, const f32x2 
     }
 }
 
-template <typename TIn, typename TDt, int R, int L, int CS>
-__global__ void __launch_bounds__(kBwdThreads, R == 4 ? 3 : 1)
-selective_scan_bwd_kernel(SelScanBwdArgs b, int units)
+// CTAs of an SM: 168 registers a thread with two sets of channels, 128 with one.
+template <int R, int CS>
+constexpr int kCtasPerSm = R > 4 ? 1 : CS == 2 ? 3 : 4;
+
+// One CTA per (unit, channel tile); with more units than CTAs per tile, a CTA
+// takes every `ctas`-th.  kCarry: the pass before, where sequences are cut
+// into segments.  It leaves the gradient of the state in front of a segment as
+// the segment's own tokens give it (the last one of a sequence: from the final
+// state's gradient), and the sum of its step sizes; the main pass folds the
+// segments behind its own.
+template <typename TIn, typename TDt, int R, int L, int CS, bool kCarry>
+__global__ void __launch_bounds__(kBwdThreads, kCtasPerSm<R, CS>)
+selective_scan_bwd_kernel(SelScanBwdArgs b, int ctas)
 {
     using S = BwdShape<R, L, CS>;
     constexpr int CB = S::CB, CL = S::CL, NP = S::NP, P = R / 2, KC = kSavedEvery;
@@ -107,7 +121,7 @@ selective_scan_bwd_kernel(SelScanBwdArgs b, int units)
     extern __shared__ __align__(16) float smem[];
     float2 *s_vu = reinterpret_cast<float2 *>(smem);
     float *s_g = smem + 2 * S::kRow, *s_B = s_g + S::kRow, *s_C = s_B + KC * NP;
-    float *s_h = s_C + KC * NP, *s_part = s_h + S::kStates;
+    float *s_h = s_C + KC * NP, *s_red = s_h + S::kStates;
     const SelScanArgs &a = b.f;
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -119,21 +133,25 @@ selective_scan_bwd_kernel(SelScanBwdArgs b, int units)
     const long T = a.cu_seqlens ? (long)a.seqlen : (long)a.nseq * a.seqlen;
 
     const int j = lane % L;
-    const int ch0 = warp * S::CW + lane / L;         // channel of set q: c0 + ch0 + q * CL
+    const int ch0 = warp * S::CW + CS * (lane / L);  // channel of set q: c0 + ch0 + q
+    const int dc = c0 + ch0;
     const int first = reduced_first<kSub, L, 1>(lane);
     const int sc = 2 * (tid % (CB / 2)), st = tid / (CB / 2), ds = c0 + sc;   // staging: channels ds, ds + 1
     const bool slive0 = ds < cend, slive1 = ds + 1 < cend;
     const f32x2 bias2 = pack2(a.dtp.bias && slive0 ? a.dtp.bias[ds] : 0.f, a.dtp.bias && slive1 ? a.dtp.bias[ds + 1] : 0.f);
     const int xs = (int)a.x_stride, vs = (int)a.dt_stride, ys = (int)b.dy_stride, zs = (int)a.z_stride;
     const int Bs = (int)a.B_stride, Cs = (int)a.C_stride;
+    // this lane's own two channels as one access (loads, and stores into rows of dim values)
+    const bool pair_in = CS == 2 && a.pairs && dc + 1 < cend, pair_out = CS == 2 && gdim % 2 == 0 && dc + 1 < cend;
+    const f32x2 own_bias = pack2(a.dtp.bias && dc < cend ? a.dtp.bias[dc] : 0.f, a.dtp.bias && CS == 2 && dc + 1 < cend ? a.dtp.bias[dc + 1] : 0.f);
+    const f32x2 own_skip = pack2(a.D && dc < cend ? a.D[dc] : 0.f, a.D && CS == 2 && dc + 1 < cend ? a.D[dc + 1] : 0.f);
     const bool whole_rows = a.pairs && cend - c0 == CB && N == NP;
 
     f32x2 A[CS][P], G[CS][P], dA[CS][P];
-    float sum_D[CS], sum_bias[CS];
+    f32x2 sum_D = pack2(0.f, 0.f), sum_bias = sum_D;  // of this lane's channel(s)
 #pragma unroll
     for (int q = 0; q < CS; ++q) {
-        const int d = c0 + ch0 + q * CL;
-        sum_D[q] = sum_bias[q] = 0.f;
+        const int d = dc + q;
 #pragma unroll
         for (int p = 0; p < P; ++p) A[q][p] = dA[q][p] = pack2(0.f, 0.f);
         if (d < cend) load_row<R>(a.A + (long)d * N, j, N, A[q]);
@@ -141,22 +159,42 @@ selective_scan_bwd_kernel(SelScanBwdArgs b, int units)
         for (int p = 0; p < P; ++p) A[q][p] = mul2(A[q][p], pack2(kLog2e, kLog2e));
     }
 
-    for (int s = unit; s < a.nseq; s += units) {
-        long lo, hi;
-        if (!seq_range(a, T, s, lo, hi)) {
-            report_status(a.status_dev, kStatusDeviceInput);
-            continue;
-        }
-        const long save0 = lo / KC + s;
+    __shared__ int s_seq;
+    if (kCarry) check_offsets(a, T);
+    const bool ranked = !a.span && a.cu_seqlens && a.nseq > 1 && a.nseq <= kMaxRanked && ctas == a.nseq;
+    for (int u = unit; u < a.units; u += ctas) {
+        Unit w;
+        if (!find_unit(a, T, ranked ? longest_first(a, u, &s_seq) : u, w)) continue;
+        if (kCarry && w.k == 0) continue;
+        const int s = w.s;
+        const long lo = w.lo, hi = w.hi, save0 = lo / KC + s;
 #pragma unroll
         for (int q = 0; q < CS; ++q) {
-            const int d = c0 + ch0 + q * CL;
+            const int d = dc + q;
 #pragma unroll
             for (int p = 0; p < P; ++p) G[q][p] = pack2(0.f, 0.f);
-            if (b.dfinal && d < cend) load_row<R>(b.dfinal + ((long)s * a.dim + d) * N, j, N, G[q]);
+            if (w.e == hi && b.dfinal && d < cend) load_row<R>(b.dfinal + ((long)s * a.dim + d) * N, j, N, G[q]);
         }
+        if (!kCarry && w.e < hi) {               // the gradient that enters from the segments behind
+            for (long m = (hi - lo - 1) / a.span; m > w.k; --m) {
+#pragma unroll
+                for (int q = 0; q < CS; ++q) {
+                    const int d = dc + q;
+                    if (d >= cend) continue;
+                    f32x2 own[P];
+                    load_row<R>(a.range_state + ((w.base + m) * a.dim + d) * N, j, N, own);
+                    const float v = a.range_dt[(w.base + m) * a.dim + d];
+#pragma unroll
+                    for (int p = 0; p < P; ++p) G[q][p] = fma2(ex2_pair(mul2(pack2(v, v), A[q][p])), G[q][p], own[p]);
+                }
+            }
+        }
+        float vsum[CS];
+#pragma unroll
+        for (int q = 0; q < CS; ++q) vsum[q] = 0.f;
 
-        for (long chunk = (hi - lo + KC - 1) / KC - 1; chunk >= 0; --chunk) {
+        const long chunk0 = (w.b - lo) / KC;
+        for (long chunk = (w.e - lo + KC - 1) / KC - 1; chunk >= chunk0; --chunk) {
             const long t0 = lo + chunk * KC;
             const int n_tok = (int)min((long)KC, hi - t0);
             // rows of the chunk's first token; everything below is a 32-bit offset from them
@@ -169,10 +207,10 @@ selective_scan_bwd_kernel(SelScanBwdArgs b, int units)
             f32x2 h[CS][P];
 #pragma unroll
             for (int q = 0; q < CS; ++q) {
-                const int d = c0 + ch0 + q * CL;
+                const int d = dc + q;
 #pragma unroll
                 for (int p = 0; p < P; ++p) h[q][p] = pack2(0.f, 0.f);
-                if (d < cend) load_row<R>(a.saved + ((save0 + chunk) * a.dim + d) * N, j, N, h[q]);
+                if (!kCarry && d < cend) load_row<R>(a.saved + ((save0 + chunk) * a.dim + d) * N, j, N, h[q]);
             }
             // stage: step sizes, v x, gated dy; B, C; zero behind the sequence's end
             constexpr int kStep = KC / RS < 4 ? (KC / RS < 1 ? 1 : KC / RS) : 4;   // tokens whose loads are in flight together
@@ -218,12 +256,61 @@ selective_scan_bwd_kernel(SelScanBwdArgs b, int units)
                 s_B[e] = ok ? ld_as<TIn>(Bt, k * Bs + n) : 0.f;
                 s_C[e] = ok ? ld_as<TIn>(Ct, k * Cs + n) : 0.f;
             }
+            // the chunk that comes next, into L2: its rows of x, dt, dy and z (a line each), and its saved state
+            if (chunk > chunk0) {
+                constexpr int kLine = 128;
+                const char *px = reinterpret_cast<const char *>(xt - (long)KC * xs), *pv = reinterpret_cast<const char *>(vt - (long)KC * vs);
+                const char *py = reinterpret_cast<const char *>(yt - (long)KC * ys), *pz = reinterpret_cast<const char *>(zt - (long)KC * zs);
+                const int row = tid % KC, which = tid / KC;     // kBwdThreads = 4 KC
+                const char *p = which == 0 ? px + (long)row * xs * (int)sizeof(TIn) : which == 1 ? pv + (long)row * vs * (int)sizeof(TDt)
+                              : which == 2 ? py + (long)row * ys * (int)sizeof(TIn) : pz + (long)row * zs * (int)sizeof(TIn);
+                if (which < 3 || a.z) prefetch_l2(p);
+                const char *ps = reinterpret_cast<const char *>(a.saved + ((save0 + chunk - 1) * a.dim + c0) * N);
+                if ((long)tid * kLine < (long)(cend - c0) * N * (long)sizeof(float)) prefetch_l2(ps + tid * kLine);
+            }
             __syncthreads();
 
             const int last = (n_tok - 1) / kSub;
+            // step sizes v and v x of token t for this lane's channels
+            auto load_vu = [&](int t, float (&v)[CS], float (&u)[CS]) {
+                if constexpr (CS == 2) {
+                    const float4 q = *reinterpret_cast<const float4 *>(&s_vu[t * CB + ch0]);
+                    v[0] = q.x; u[0] = q.y; v[1] = q.z; u[1] = q.w;
+                } else {
+                    const float2 q = s_vu[t * CB + ch0];
+                    v[0] = q.x; u[0] = q.y;
+                }
+            };
+            auto load_g = [&](int t, float (&g)[CS]) {
+                if constexpr (CS == 2) {
+                    const float2 q = *reinterpret_cast<const float2 *>(&s_g[t * CB + ch0]);
+                    g[0] = q.x; g[1] = q.y;
+                } else {
+                    g[0] = s_g[t * CB + ch0];
+                }
+            };
+            if constexpr (kCarry) {
+#pragma unroll 4
+                for (int t = n_tok - 1; t >= 0; --t) {
+                    f32x2 C[P];
+                    float v[CS], u[CS], g[CS];
+                    lds_pairs(s_C + t * NP + j * R, C);
+                    load_vu(t, v, u);
+                    load_g(t, g);
+#pragma unroll
+                    for (int q = 0; q < CS; ++q) {
+                        vsum[q] += v[q];
+#pragma unroll
+                        for (int p = 0; p < P; ++p)
+                            G[q][p] = mul2(ex2_pair(mul2(pack2(v[q], v[q]), A[q][p])), fma2(pack2(g[q], g[q]), C[p], G[q][p]));
+                    }
+                }
+                __syncthreads();
+                continue;
+            }
             // forward: the state in front of every sub-tile
 #pragma unroll 1
-            for (int sub = 0; sub <= last; ++sub) {
+            for (int sub = 0; sub < last; ++sub) {
 #pragma unroll
                 for (int q = 0; q < CS; ++q) {
                     float *slot = s_h + ((sub * CS + q) * kBwdThreads + tid) * R;
@@ -231,67 +318,82 @@ selective_scan_bwd_kernel(SelScanBwdArgs b, int units)
                     for (int p = 0; p < P; p += 2)
                         *reinterpret_cast<ulonglong2 *>(slot + 2 * p) = make_ulonglong2(h[q][p].v, h[q][p + 1].v);
                 }
-                if (sub == last) break;
 #pragma unroll
                 for (int k = 0; k < kSub; ++k) {
                     const int t = sub * kSub + k;
                     f32x2 B[P];
+                    float v[CS], u[CS];
                     lds_pairs(s_B + t * NP + j * R, B);
+                    load_vu(t, v, u);
 #pragma unroll
-                    for (int q = 0; q < CS; ++q) {
-                        const float2 vu = s_vu[t * CB + ch0 + q * CL];
+                    for (int q = 0; q < CS; ++q)
 #pragma unroll
                         for (int p = 0; p < P; ++p)
-                            h[q][p] = fma2(ex2_pair(mul2(pack2(vu.x, vu.x), A[q][p])), h[q][p], mul2(pack2(vu.y, vu.y), B[p]));
-                    }
+                            h[q][p] = fma2(ex2_pair(mul2(pack2(v[q], v[q]), A[q][p])), h[q][p], mul2(pack2(u[q], u[q]), B[p]));
                 }
             }
 
 #pragma unroll 1
             for (int sub = last; sub >= 0; --sub) {
+                // inputs of the tokens that this lane finishes
+                uint32_t rv[kLeft][2], rx[kLeft][2], rg[kLeft][2], rz[kLeft][2];
+                bool mine[kLeft];
+#pragma unroll
+                for (int i = 0; i < kLeft; ++i) {
+                    const int t = sub * kSub + first + i;
+                    mine[i] = t < n_tok && dc < cend && j % kSame == 0;
+#pragma unroll
+                    for (int w = 0; w < 2; ++w) rv[i][w] = rx[i][w] = rg[i][w] = rz[i][w] = 0u;
+                    if (!mine[i]) continue;
+                    if (pair_in) {
+                        pair_load(vt, t * vs + ch0, rv[i]);
+                        pair_load(xt, t * xs + ch0, rx[i]);
+                        if (a.z) {
+                            pair_load(yt, t * ys + ch0, rg[i]);
+                            pair_load(zt, t * zs + ch0, rz[i]);
+                        }
+                    } else {
+#pragma unroll
+                        for (int w = 0; w < CS; ++w) {
+                            if (dc + w >= cend) break;
+                            rv[i][w] = raw_load<TDt>(vt, t * vs + ch0 + w);
+                            rx[i][w] = raw_load<TIn>(xt, t * xs + ch0 + w);
+                            if (a.z) {
+                                rg[i][w] = raw_load<TIn>(yt, t * ys + ch0 + w);
+                                rz[i][w] = raw_load<TIn>(zt, t * zs + ch0 + w);
+                            }
+                        }
+                    }
+                }
                 f32x2 dB[kSub][P], dC[kSub][P], B[kSub][P], C[kSub][P];
+                float v[kSub][CS], u[kSub][CS], g[kSub][CS];
 #pragma unroll
                 for (int k = 0; k < kSub; ++k) {
                     lds_pairs(s_B + (sub * kSub + k) * NP + j * R, B[k]);
                     lds_pairs(s_C + (sub * kSub + k) * NP + j * R, C[k]);
+                    load_vu(sub * kSub + k, v[k], u[k]);
+                    load_g(sub * kSub + k, g[k]);
                 }
+                float ys_[CS][kSub], ws_[CS][kSub], qs_[CS][kSub];
 #pragma unroll
                 for (int q = 0; q < CS; ++q) {
-                    const int ch = ch0 + q * CL, d = c0 + ch;
-                    // inputs of the tokens that this lane finishes
-                    uint32_t rv[kLeft], rx[kLeft], rg[kLeft], rz[kLeft];
-                    bool mine[kLeft];
-#pragma unroll
-                    for (int i = 0; i < kLeft; ++i) {
-                        const int t = sub * kSub + first + i;
-                        mine[i] = t < n_tok && d < cend && j % kSame == 0;
-                        rv[i] = rx[i] = rg[i] = rz[i] = 0u;
-                        if (mine[i]) {
-                            rv[i] = raw_load<TDt>(vt, t * vs + ch);
-                            rx[i] = raw_load<TIn>(xt, t * xs + ch);
-                            if (a.z) {
-                                rg[i] = raw_load<TIn>(yt, t * ys + ch);
-                                rz[i] = raw_load<TIn>(zt, t * zs + ch);
-                            }
-                        }
-                    }
                     f32x2 hh[kSub + 1][P], aa[kSub][P];
-                    lds_pairs(s_h + ((sub * CS + q) * kBwdThreads + tid) * R, hh[0]);
-                    float2 vu[kSub];
+                    if (sub == last) {
 #pragma unroll
-                    for (int k = 0; k < kSub; ++k) {
-                        vu[k] = s_vu[(sub * kSub + k) * CB + ch];
+                        for (int p = 0; p < P; ++p) hh[0][p] = h[q][p];
+                    } else {
+                        lds_pairs(s_h + ((sub * CS + q) * kBwdThreads + tid) * R, hh[0]);
+                    }
+#pragma unroll
+                    for (int k = 0; k < kSub; ++k)
 #pragma unroll
                         for (int p = 0; p < P; ++p) {
-                            aa[k][p] = ex2_pair(mul2(pack2(vu[k].x, vu[k].x), A[q][p]));
-                            hh[k + 1][p] = fma2(aa[k][p], hh[k][p], mul2(pack2(vu[k].y, vu[k].y), B[k][p]));
+                            aa[k][p] = ex2_pair(mul2(pack2(v[k][q], v[k][q]), A[q][p]));
+                            hh[k + 1][p] = fma2(aa[k][p], hh[k][p], mul2(pack2(u[k][q], u[k][q]), B[k][p]));
                         }
-                    }
-                    float yv[kSub], wv[kSub], qv[kSub];
 #pragma unroll
                     for (int k = kSub - 1; k >= 0; --k) {
-                        const float g = s_g[(sub * kSub + k) * CB + ch];
-                        const f32x2 vv = pack2(vu[k].x, vu[k].x), uu = pack2(vu[k].y, vu[k].y), gg = pack2(g, g);
+                        const f32x2 vv = pack2(v[k][q], v[k][q]), uu = pack2(u[k][q], u[k][q]), gg = pack2(g[k][q], g[k][q]);
                         f32x2 ya, wa, qa;
 #pragma unroll
                         for (int p = 0; p < P; ++p) {
@@ -305,101 +407,121 @@ selective_scan_bwd_kernel(SelScanBwdArgs b, int units)
                             dC[k][p] = q ? fma2(hh[k + 1][p], gg, dC[k][p]) : mul2(hh[k + 1][p], gg);
                             dB[k][p] = q ? fma2(dh, uu, dB[k][p]) : mul2(dh, uu);
                         }
-                        yv[k] = sum2(ya);
-                        wv[k] = sum2(wa);
-                        qv[k] = sum2(qa);
+                        ys_[q][k] = sum2(ya);
+                        ws_[q][k] = sum2(wa);
+                        qs_[q][k] = sum2(qa);
                     }
-                    reduce_lanes<kSub, L, 1>(yv, lane);
-                    reduce_lanes<kSub, L, 1>(wv, lane);
-                    reduce_lanes<kSub, L, 1>(qv, lane);
-                    const float bias = a.dtp.bias && d < cend ? __ldg(a.dtp.bias + d) : 0.f;
-                    const float skip = a.D && d < cend ? __ldg(a.D + d) : 0.f;
-#pragma unroll
-                    for (int i = 0; i < kLeft; ++i) {
-                        if (!mine[i]) continue;
-                        const int t = sub * kSub + first + i;
-                        const long o = t0 * a.dim + c0;
-                        const int oo = t * a.dim + ch;
-                        const float x = raw_value<TIn>(rx[i]), v = s_vu[t * CB + ch].x, g = s_g[t * CB + ch];
-                        if (a.z) {
-                            const float z = raw_value<TIn>(rz[i]);
-                            const float sg = rcp_approx(1.f + ex2_approx(-z * kLog2e));
-                            store_out(static_cast<TIn *>(b.dz) + o + oo,
-                                      raw_value<TIn>(rg[i]) * fmaf(skip, x, yv[i]) * sg * fmaf(z, 1.f - sg, 1.f));
-                        }
-                        const float ddt = fmaf(qv[i], kLn2, wv[i] * x) * dt_slope(a.dtp, raw_value<TDt>(rv[i]), bias);
-                        store_out(static_cast<TIn *>(b.dx) + o + oo, fmaf(wv[i], v, skip * g));
-                        store_out(static_cast<TDt *>(b.ddt) + o + oo, ddt);
-                        sum_D[q] = fmaf(g, x, sum_D[q]);
-                        sum_bias[q] += ddt;
-                    }
+                    reduce_lanes<kSub, L, 1>(ys_[q], lane);
+                    reduce_lanes<kSub, L, 1>(ws_[q], lane);
+                    reduce_lanes<kSub, L, 1>(qs_[q], lane);
                 }
-                // dB, dC of the sub-tile: over the warp's channels, then the CTA's warps
-                float *part = s_part + (sub & 1) * (2 * kWarps * kSub * NP);
 #pragma unroll
-                for (int w = 0; w < 2; ++w) {
-                    float f[kSub * R];
-#pragma unroll
-                    for (int k = 0; k < kSub; ++k)
-#pragma unroll
-                        for (int p = 0; p < P; ++p) {
-                            f[k * R + 2 * p] = w ? lo2(dC[k][p]) : lo2(dB[k][p]);
-                            f[k * R + 2 * p + 1] = w ? hi2(dC[k][p]) : hi2(dB[k][p]);
-                        }
-                    const int f0 = reduce_lanes<kSub * R, CL, L>(f, lane);
-                    constexpr int kVals = reduce_left(kSub * R, CL);
-                    constexpr int kCopies = CL > kSub * R ? CL / (kSub * R) : 1;
-                    if ((lane / L) % kCopies == 0) {
-#pragma unroll
-                        for (int i = 0; i < kVals; ++i) {
-                            const int k = (f0 + i) / R, r = (f0 + i) % R;
-                            part[((w * kWarps + warp) * kSub + k) * NP + j * R + r] = f[i];
-                        }
+                for (int i = 0; i < kLeft; ++i) {
+                    if (!mine[i]) continue;
+                    constexpr int q1 = CS - 1;                 // CS == 1: the second half repeats the first and is not stored
+                    const int t = sub * kSub + first + i;
+                    float tv[CS], tu[CS], tg[CS];
+                    load_vu(t, tv, tu);
+                    load_g(t, tg);
+                    const f32x2 x = pair_value<TIn>(rx[i]), vv = pack2(tv[0], tv[q1]), gg = pack2(tg[0], tg[q1]);
+                    const f32x2 w = pack2(ws_[0][i], ws_[q1][i]), y = pack2(ys_[0][i], ys_[q1][i]), qq = pack2(qs_[0][i], qs_[q1][i]);
+                    const long o = (t0 + t) * a.dim + dc;
+                    const f32x2 dx = fma2(w, vv, mul2(own_skip, gg));
+                    const f32x2 ddt = mul2(fma2(qq, pack2(kLn2, kLn2), mul2(w, x)), dt_slope2(a.dtp, pair_value<TDt>(rv[i]), own_bias));
+                    store_pair(static_cast<TIn *>(b.dx) + o, dx, pair_out, CS == 2 && dc + 1 < cend);
+                    store_pair(static_cast<TDt *>(b.ddt) + o, ddt, pair_out, CS == 2 && dc + 1 < cend);
+                    if (a.z) {
+                        const f32x2 z = pair_value<TIn>(rz[i]), one = pack2(1.f, 1.f);
+                        const f32x2 e = add2(ex2_pair(mul2(z, pack2(-kLog2e, -kLog2e))), one);
+                        const f32x2 sg = pack2(rcp_approx(lo2(e)), rcp_approx(hi2(e)));
+                        const f32x2 slope = mul2(sg, fma2(z, fma2(sg, pack2(-1.f, -1.f), one), one));
+                        store_pair(static_cast<TIn *>(b.dz) + o, mul2(mul2(pair_value<TIn>(rg[i]), fma2(own_skip, x, y)), slope),
+                                   pair_out, CS == 2 && dc + 1 < cend);
                     }
+                    sum_D = fma2(gg, x, sum_D);
+                    sum_bias = add2(sum_bias, ddt);
                 }
+                // dB, dC of the sub-tile, summed over the CTA's channels: every thread leaves its own, and
+                // thread (warp k, lane: state group j, which of dB and dC, part) adds those of token k from
+                // the threads of its part; the parts are added by shuffles
+                if (sub != last) __syncthreads();              // the sums of the sub-tile before have been read
+                float *mine_red = s_red + tid * S::kPitch;
+#pragma unroll
+                for (int k = 0; k < kSub; ++k)
+#pragma unroll
+                    for (int p = 0; p < P; p += 2) {
+                        *reinterpret_cast<ulonglong2 *>(mine_red + k * R + 2 * p) = make_ulonglong2(dB[k][p].v, dB[k][p + 1].v);
+                        *reinterpret_cast<ulonglong2 *>(mine_red + (kSub + k) * R + 2 * p) = make_ulonglong2(dC[k][p].v, dC[k][p + 1].v);
+                    }
                 __syncthreads();
-                float *oB = b.part_B + (((long)gtile * T + t0 + sub * kSub) * a.ngroups + grp) * N;
-                float *oC = b.part_C + (((long)gtile * T + t0 + sub * kSub) * a.ngroups + grp) * N;
-                for (int e = tid; e < 2 * kSub * NP; e += kBwdThreads) {
-                    const int w = e / (kSub * NP), k = (e / NP) % kSub, n = e % NP;
-                    float sum = 0.f;
+                constexpr int kPartsN = L < 16 ? 16 / L : 1, kFrom = kBwdThreads / L / kPartsN;
+                static_assert(kWarps == kSub, "a warp adds one token of the sub-tile");
 #pragma unroll
-                    for (int i = 0; i < kWarps; ++i) sum += part[((w * kWarps + i) * kSub + k) * NP + n];
-                    if (sub * kSub + k < n_tok && n < N) (w ? oC : oB)[k * a.ngroups * N + n] = sum;
+                for (int it = 0; it < (L == 32 ? 2 : 1) * (R / 4); ++it) {
+                    const int combo = L == 32 ? lane + 32 * (it % 2) : lane % (2 * L), r4 = 4 * (L == 32 ? it / 2 : it);
+                    const int cj = combo % L, w = combo / L, part = L == 32 ? 0 : lane / (2 * L);
+                    f32x2 s01 = pack2(0.f, 0.f), s23 = s01;
+#pragma unroll
+                    for (int i = 0; i < kFrom; ++i) {
+                        const int m = part * kFrom + i, from = m / CL * 32 + m % CL * L + cj;
+                        f32x2 f[2];
+                        lds_pairs(s_red + from * S::kPitch + (w * kSub + warp) * R + r4, f);
+                        s01 = add2(s01, f[0]);
+                        s23 = add2(s23, f[1]);
+                    }
+                    float f[4] = {lo2(s01), hi2(s01), lo2(s23), hi2(s23)};
+                    const int f0 = reduce_lanes<4, kPartsN, (L < 16 ? 2 * L : 32)>(f, lane);
+                    constexpr int kOut = reduce_left(4, kPartsN), kDup = kPartsN > 4 ? kPartsN / 4 : 1;
+                    const int t = sub * kSub + warp;
+                    if (t >= n_tok || part % kDup) continue;
+                    float *out = (w ? b.part_C : b.part_B) + (((long)gtile * T + t0 + t) * a.ngroups + grp) * N + cj * R + r4 + f0;
+#pragma unroll
+                    for (int i = 0; i < kOut; ++i)
+                        if (cj * R + r4 + f0 + i < N) out[i] = f[i];
                 }
             }
-            // the last sub-tile's barrier lies behind every read of the staged chunk: the next may be staged
+            // the last sub-tile's second barrier lies behind every read of the staged chunk, so the next may be
+            // staged; its sums are read before the barrier that follows the staging
         }
-        if (b.dinitial) {
+        if (kCarry) {
 #pragma unroll
             for (int q = 0; q < CS; ++q) {
-                const int d = c0 + ch0 + q * CL;
+                const int d = dc + q;
+                if (d >= cend) continue;
+                store_row<R>(a.range_state + ((long)u * a.dim + d) * N, j, N, G[q]);
+                if (j == 0) a.range_dt[(long)u * a.dim + d] = vsum[q];
+            }
+        } else if (b.dinitial && w.k == 0) {
+#pragma unroll
+            for (int q = 0; q < CS; ++q) {
+                const int d = dc + q;
                 if (d < cend) store_row<R>(b.dinitial + ((long)s * a.dim + d) * N, j, N, G[q]);
             }
         }
     }
 
+    if (kCarry) return;
+#pragma unroll
+    for (int o = L / 2; o > 0; o >>= 1) {
+        sum_D = add2(sum_D, pack2(__shfl_xor_sync(0xffffffffu, lo2(sum_D), o), __shfl_xor_sync(0xffffffffu, hi2(sum_D), o)));
+        sum_bias = add2(sum_bias, pack2(__shfl_xor_sync(0xffffffffu, lo2(sum_bias), o), __shfl_xor_sync(0xffffffffu, hi2(sum_bias), o)));
+    }
 #pragma unroll
     for (int q = 0; q < CS; ++q) {
-        const int d = c0 + ch0 + q * CL;
-#pragma unroll
-        for (int o = L / 2; o > 0; o >>= 1) {
-            sum_D[q] += __shfl_xor_sync(0xffffffffu, sum_D[q], o);
-            sum_bias[q] += __shfl_xor_sync(0xffffffffu, sum_bias[q], o);
-        }
+        const int d = dc + q;
         if (d >= cend) continue;
         store_row<R>(b.part_A + ((long)unit * a.dim + d) * N, j, N, dA[q]);
         if (j == 0) {
-            b.part_D[(long)unit * a.dim + d] = sum_D[q];
-            b.part_bias[(long)unit * a.dim + d] = sum_bias[q];
+            b.part_D[(long)unit * a.dim + d] = q ? hi2(sum_D) : lo2(sum_D);
+            b.part_bias[(long)unit * a.dim + d] = q ? hi2(sum_bias) : lo2(sum_bias);
         }
     }
 }
 
 // Sums of the parts: dB and dC over the channel tiles of a group, dA, dD and
-// ddt_bias over the units.
+// ddt_bias over the CTAs of a tile.
 __global__ void __launch_bounds__(256)
-selective_scan_bwd_sum_kernel(SelScanBwdArgs b, int gtiles, int units, long nB, long nA)
+selective_scan_bwd_sum_kernel(SelScanBwdArgs b, int gtiles, int ctas, long nB, long nA)
 {
     const SelScanArgs &a = b.f;
     long i = (long)blockIdx.x * 256 + threadIdx.x;
@@ -433,81 +555,148 @@ selective_scan_bwd_sum_kernel(SelScanBwdArgs b, int gtiles, int units, long nB, 
     }
     if (!out) return;
     float s = 0.f;
-    for (int q = 0; q < units; ++q) s += p[q * n + i];
+    for (int q = 0; q < ctas; ++q) s += p[q * n + i];
     out[i] = s;
 }
 
 struct BwdPlan {
-    int cs, cb, units, gtiles;
-    long tokens;
-    size_t bytes_B, bytes_A, bytes_D;
+    int cs, gtiles, ctas, units, span;
+    size_t bytes_B, bytes_A, bytes_D, bytes_carry;
+    size_t bytes() const { return 2 * bytes_B + bytes_A + 2 * bytes_D + bytes_carry; }
 };
 
 template <typename TIn, typename TDt, int R, int L, int CS>
-cudaError_t launch_shape(SelScanBwdArgs b, const BwdPlan &p, cudaStream_t stream)
+cudaError_t launch_shape(const SelScanBwdArgs &b, const BwdPlan &p, cudaStream_t stream)
 {
     using S = BwdShape<R, L, CS>;
-    const cudaError_t e = cudaFuncSetAttribute(selective_scan_bwd_kernel<TIn, TDt, R, L, CS>,
+    const cudaError_t e = cudaFuncSetAttribute(selective_scan_bwd_kernel<TIn, TDt, R, L, CS, false>,
                                                cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::kBytes);
     if (e) return e;
-    const long long blocks = (long long)p.gtiles * b.f.ngroups * p.units;
-    if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
-    selective_scan_bwd_kernel<TIn, TDt, R, L, CS><<<(unsigned)blocks, kBwdThreads, S::kBytes, stream>>>(b, p.units);
+    const long long tiles = (long long)p.gtiles * b.f.ngroups;
+    if (tiles * p.units > 0x7fffffffLL) return cudaErrorInvalidValue;
+    if (p.span) {
+        const cudaError_t e2 = cudaFuncSetAttribute(selective_scan_bwd_kernel<TIn, TDt, R, L, CS, true>,
+                                                    cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::kStaged);
+        if (e2) return e2;
+        selective_scan_bwd_kernel<TIn, TDt, R, L, CS, true><<<(unsigned)(tiles * p.units), kBwdThreads, S::kStaged, stream>>>(b, p.units);
+    }
+    selective_scan_bwd_kernel<TIn, TDt, R, L, CS, false><<<(unsigned)(tiles * p.ctas), kBwdThreads, S::kBytes, stream>>>(b, p.ctas);
     return cudaGetLastError();
 }
 
 // Lanes per channel for d_state (R = 4 states a lane, 8 above 128).
 int lanes_for(int N) { return N <= 4 ? 1 : N <= 8 ? 2 : N <= 16 ? 4 : N <= 32 ? 8 : N <= 64 ? 16 : 32; }
 
+int sm_count()
+{
+    int dev = 0, sms = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms <= 0) {
+        cudaGetLastError();
+        return 148;
+    }
+    return sms;
+}
+
+// Time of `ctas` equal CTAs, `per` to an SM, in rounds: a last round with fewer
+// to an SM runs faster, but not in proportion (share[k]: k CTAs an SM against a
+// full one).
+double rounds(long long ctas, int sms, int per, const double *share)
+{
+    const long long full = ctas / ((long long)sms * per), rest = ctas - full * sms * per;
+    return (double)full + share[(rest + sms - 1) / sms];
+}
+
 BwdPlan make_plan(int nseq, long T, int dim, int d_state, int ngroups)
 {
     BwdPlan p{};
-    const int L = lanes_for(d_state);
-    p.tokens = T;
-    p.units = nseq < kMaxUnits ? nseq : kMaxUnits;
-    p.cs = L == 1 || d_state > 128 ? 1 : 2;
-    p.cb = 32 / L * p.cs * kWarps;
-    p.gtiles = (dim / ngroups + p.cb - 1) / p.cb;
+    const int L = lanes_for(d_state), gdim = dim / ngroups, sms = sm_count();
+    auto tiles_of = [&](int cs) { const int cb = 32 / L * cs * kWarps; return (gdim + cb - 1) / cb; };
+    // Segments, where one-set CTAs of whole sequences do not fill a third of the device: as many as fill it,
+    // of at least 128 tokens.  The pass before costs about a quarter of the work again.
+    const long long ctas = (long long)tiles_of(1) * ngroups * nseq;
+    p.units = nseq;
+    if (ctas * 3 < 4LL * sms) {
+        long segments = (long)(4LL * sms / ((long long)tiles_of(1) * ngroups));
+        if (segments > T / 128) segments = T / 128;
+        if (segments > 256) segments = 256;
+        if (segments >= 2 && segments > nseq + nseq / 2) {
+            const long n = (T + segments - 1) / segments;
+            p.span = (int)((n + kSavedEvery - 1) / kSavedEvery * kSavedEvery);
+            p.units = (int)(T / p.span + nseq);
+        }
+    }
+    p.ctas = p.span || p.units < kMaxCtas ? p.units : kMaxCtas;
+    // One or two sets of channels a warp: two share the loads of B and C and the sums over the channels (a
+    // quarter less time an element when the device is full), one makes twice as many CTAs.  4 x 2048 tokens of
+    // 8192 channels with 16 states: 512 CTAs of two sets leave 68 for a second round, 2.41 ms, against 2.27 ms
+    // for 1024 of one; 16 x 512 tokens: 1.79 against 2.16 ms.
+    p.cs = 1;
+    if (L > 1 && d_state <= 128) {
+        static const double share1[] = {0., 0.5, 0.68, 0.84, 1.}, share2[] = {0., 0.6, 0.75, 1.};
+        const double one = rounds((long long)tiles_of(1) * ngroups * p.ctas, sms, 4, share1);
+        const double two = 1.22 * rounds((long long)tiles_of(2) * ngroups * p.ctas, sms, 3, share2);
+        if (two < one) p.cs = 2;
+    }
+    p.gtiles = tiles_of(p.cs);
     auto up = [](size_t v) { return (v + 15) / 16 * 16; };
+    const size_t row = (size_t)dim * sizeof(float);
     p.bytes_B = up((size_t)p.gtiles * T * ngroups * d_state * sizeof(float));
-    p.bytes_A = up((size_t)p.units * dim * d_state * sizeof(float));
-    p.bytes_D = up((size_t)p.units * dim * sizeof(float));
+    p.bytes_A = up(p.ctas * row * d_state);
+    p.bytes_D = up(p.ctas * row);
+    p.bytes_carry = p.span ? p.units * row * d_state + up(p.units * row) : 0;
     return p;
+}
+
+template <typename TIn, typename TDt, int R, int L>
+cudaError_t launch_sets(const SelScanBwdArgs &b, const BwdPlan &p, cudaStream_t stream)
+{
+    if constexpr (R == 4 && L > 1)
+        if (p.cs == 2) return launch_shape<TIn, TDt, R, L, 2>(b, p, stream);
+    return launch_shape<TIn, TDt, R, L, 1>(b, p, stream);
 }
 
 template <typename TIn, typename TDt>
 cudaError_t launch_types(const SelScanBwdArgs &b, const BwdPlan &p, cudaStream_t stream)
 {
     const int N = b.f.d_state;
-    if (N <= 4) return launch_shape<TIn, TDt, 4, 1, 1>(b, p, stream);
-    if (N <= 8) return launch_shape<TIn, TDt, 4, 2, 2>(b, p, stream);
-    if (N <= 16) return launch_shape<TIn, TDt, 4, 4, 2>(b, p, stream);
-    if (N <= 32) return launch_shape<TIn, TDt, 4, 8, 2>(b, p, stream);
-    if (N <= 64) return launch_shape<TIn, TDt, 4, 16, 2>(b, p, stream);
-    if (N <= 128) return launch_shape<TIn, TDt, 4, 32, 2>(b, p, stream);
-    return launch_shape<TIn, TDt, 8, 32, 1>(b, p, stream);
+    if (N <= 4) return launch_sets<TIn, TDt, 4, 1>(b, p, stream);
+    if (N <= 8) return launch_sets<TIn, TDt, 4, 2>(b, p, stream);
+    if (N <= 16) return launch_sets<TIn, TDt, 4, 4>(b, p, stream);
+    if (N <= 32) return launch_sets<TIn, TDt, 4, 8>(b, p, stream);
+    if (N <= 64) return launch_sets<TIn, TDt, 4, 16>(b, p, stream);
+    if (N <= 128) return launch_sets<TIn, TDt, 4, 32>(b, p, stream);
+    return launch_sets<TIn, TDt, 8, 32>(b, p, stream);
 }
 
 }  // namespace
 
 size_t selective_scan_bwd_workspace(int nseq, long T, int dim, int d_state, int ngroups)
 {
-    const BwdPlan p = make_plan(nseq, T, dim, d_state, ngroups);
-    return 2 * p.bytes_B + p.bytes_A + 2 * p.bytes_D;
+    return make_plan(nseq, T, dim, d_state, ngroups).bytes();
 }
 
 cudaError_t launch_selective_scan_bwd(SelScanBwdArgs b, void *workspace, cudaStream_t stream)
 {
-    const SelScanArgs &a = b.f;
+    SelScanArgs &a = b.f;
     const long T = a.cu_seqlens ? (long)a.seqlen : (long)a.nseq * a.seqlen;
     const int N = a.d_state;
     const BwdPlan p = make_plan(a.nseq, T, a.dim, N, a.ngroups);
     char *w = static_cast<char *>(workspace);
-    b.part_B = reinterpret_cast<float *>(w);
-    b.part_C = reinterpret_cast<float *>(w + p.bytes_B);
-    b.part_A = reinterpret_cast<float *>(w + 2 * p.bytes_B);
-    b.part_D = reinterpret_cast<float *>(w + 2 * p.bytes_B + p.bytes_A);
-    b.part_bias = reinterpret_cast<float *>(w + 2 * p.bytes_B + p.bytes_A + p.bytes_D);
+    auto take = [&](size_t bytes) {
+        float *f = reinterpret_cast<float *>(w);
+        w += bytes;
+        return f;
+    };
+    b.part_B = take(p.bytes_B);
+    b.part_C = take(p.bytes_B);
+    b.part_A = take(p.bytes_A);
+    b.part_D = take(p.bytes_D);
+    b.part_bias = take(p.bytes_D);
+    a.span = p.span;
+    a.units = p.units;
+    a.range_state = p.span ? take((size_t)p.units * a.dim * N * sizeof(float)) : nullptr;
+    a.range_dt = p.span ? take(0) : nullptr;
     const cudaError_t e = !a.in_bf16 ? launch_types<float, float>(b, p, stream)
         : a.dt_bf16 ? launch_types<__nv_bfloat16, __nv_bfloat16>(b, p, stream)
                     : launch_types<__nv_bfloat16, float>(b, p, stream);
@@ -515,7 +704,7 @@ cudaError_t launch_selective_scan_bwd(SelScanBwdArgs b, void *workspace, cudaStr
     const long nB = T * a.ngroups * N, nA = (long)a.dim * N;
     const long long blocks = (2 * nB + nA + 2L * a.dim + 255) / 256;
     if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
-    selective_scan_bwd_sum_kernel<<<(unsigned)blocks, 256, 0, stream>>>(b, p.gtiles, p.units, nB, nA);
+    selective_scan_bwd_sum_kernel<<<(unsigned)blocks, 256, 0, stream>>>(b, p.gtiles, p.ctas, nB, nA);
     return cudaGetLastError();
 }
 

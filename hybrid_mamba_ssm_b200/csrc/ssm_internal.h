@@ -159,12 +159,11 @@ struct SelScanArgs {
     void *y;                      // [T][dim]
     float *saved;                 // [saved_rows][dim][d_state] or nullptr
     int *status_dev;
-    // Long sequences on few channels: the token stream cut into `ranges`
-    // ranges of `span` tokens; their local end states and sums of dt
-    // ([ranges][dim][d_state] and [ranges][dim]), and copies of the initial
-    // states of sequences that cross a cut ([ranges][dim][d_state]).
-    // ranges == 0: not cut.
-    int ranges, span;
+    // Long sequences on few channels: sequences cut into segments of `span`
+    // tokens, `units` of them at most (units without segments: nseq).  The
+    // segments' local end states and sums of step sizes ([units][dim][d_state]
+    // and [units][dim]), and a copy of the initial states ([nseq][dim][d_state]).
+    int span, units;
     float *range_state, *range_initial, *range_dt;
 };
 // States are saved for the backward pass every kSavedEvery tokens of a
@@ -183,10 +182,10 @@ struct SelScanBwdArgs {
     float *dA, *dD, *ddt_bias, *dinitial;   // dD, ddt_bias, dinitial may be nullptr
     // partial sums: per channel tile of a group, and per sequence
     float *part_B, *part_C;       // [tiles][T][ngroups][d_state]
-    float *part_A;                // [nseq][dim][d_state]
-    float *part_D, *part_bias;    // [nseq][dim]
+    float *part_A;                // [CTAs per tile][dim][d_state]
+    float *part_D, *part_bias;    // [CTAs per tile][dim]
 };
-int selective_scan_ranges(int nseq, long T, int dim, int d_state, int ngroups, int *span);
+int selective_scan_segments(int nseq, long T, int dim, int d_state, int ngroups, int *span);
 cudaError_t launch_selective_scan(const SelScanArgs &a, cudaStream_t stream);
 size_t selective_scan_bwd_workspace(int nseq, long T, int dim, int d_state, int ngroups);
 cudaError_t launch_selective_scan_bwd(SelScanBwdArgs a, void *workspace, cudaStream_t stream);

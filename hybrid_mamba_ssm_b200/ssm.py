@@ -765,7 +765,7 @@ def selective_scan_fwd(x, dt, A, B, C, D=None, z=None, initial_state=None, cu_se
         run in concurrent ranges.
     Returns (y, final_state), or (y, final_state, saved) with save_states.
     """
-    if stream is None and workspace == "auto" and y_dtype is None:
+    if stream is None and isinstance(workspace, str) and workspace == "auto" and y_dtype is None:
         out = _marshal.scan_fwd(x, cu_seqlens, dt, A, B, C, D, z, dt_bias, dt_softplus, dt_limit, initial_state,
                                 final_state, slot_idx, has_initial_state, y, return_final_state, save_states, status)
         if _plain(out, "selective_scan_fwd"):
@@ -784,13 +784,9 @@ def selective_scan_fwd(x, dt, A, B, C, D=None, z=None, initial_state=None, cu_se
             final_state = x.new_empty((nseq, dim, N), dtype=_F32)
         if y is None:
             y = x.new_empty(x.shape, dtype=y_dtype or x.dtype)
-        saved = ws = ws_ptr = None
-        ws_bytes = 0
-        if save_states:
-            saved = x.new_empty(lib.selective_scan_saved_size(nseq, T, dim, N) // 4, dtype=_F32)
-        else:
-            size = lib.selective_scan_workspace_size(nseq, T, dim, N, G) if workspace == "auto" else 0
-            ws, ws_ptr, ws_bytes = _workspace(workspace, size, x, dev)
+        saved = x.new_empty(lib.selective_scan_saved_size(nseq, T, dim, N) // 4, dtype=_F32) if save_states else None
+        size = lib.selective_scan_workspace_size(nseq, T, dim, N, G) if isinstance(workspace, str) else 0
+        ws, ws_ptr, ws_bytes = _workspace(workspace, size, x, dev)
         st = lib.selective_scan_fwd(
             nseq, seqlen, _addr(cu_seqlens), dim, N, G, in_code, *operands,
             _dev_like(initial_state, "initial_state", dev, _F32, (rows, dim, N)),
@@ -834,7 +830,7 @@ def selective_scan_bwd(dy, x, dt, A, B, C, saved, D=None, z=None, dfinal_state=N
     save_states=True (`saved` is its third result).  dy : like x.
     dfinal_state : [nseq, dim, d_state] fp32 or None.  The gradients have their
     inputs' shapes and types (contiguous)."""
-    if stream is None and workspace == "auto":
+    if stream is None and isinstance(workspace, str) and workspace == "auto":
         out = _marshal.scan_bwd(x, cu_seqlens, dt, A, B, C, D, z, dt_bias, dt_softplus, dt_limit, dy, saved,
                                 dfinal_state, want_dinitial, status)
         if _plain(out, "selective_scan_bwd"):
@@ -854,7 +850,7 @@ def selective_scan_bwd(dy, x, dt, A, B, C, saved, D=None, z=None, dfinal_state=N
             None if D is None else new((dim,), dtype=_F32), None if z is None else new(z.shape),
             None if dt_bias is None else new((dim,), dtype=_F32),
             new((nseq, dim, N), dtype=_F32) if want_dinitial else None)
-        size = lib.selective_scan_bwd_workspace_size(nseq, T, dim, N, G) if workspace == "auto" else 0
+        size = lib.selective_scan_bwd_workspace_size(nseq, T, dim, N, G) if isinstance(workspace, str) else 0
         ws, ws_ptr, ws_bytes = _workspace(workspace, size, x, dev)
         st = lib.selective_scan_bwd(
             nseq, seqlen, _addr(cu_seqlens), dim, N, G, in_code, dy.data_ptr(), dys, *operands,
@@ -911,7 +907,7 @@ def causal_conv1d_bwd(dy, x, weight, bias=None, initial_state=None, dfinal_state
     its conv_state), or None; dfinal_state : gradient of the states it left, or
     None.  Returns (dx, dweight, dbias, dinitial_state); dbias is None without
     bias, dinitial_state None without initial_state."""
-    if stream is None and workspace == "auto":
+    if stream is None and isinstance(workspace, str) and workspace == "auto":
         out = _marshal.conv1d_bwd(x, cu_seqlens, dy, weight, bias, initial_state, dfinal_state,
                                   _activation(activation), status)
         if _plain(out, "causal_conv1d_bwd"):
@@ -927,7 +923,7 @@ def causal_conv1d_bwd(dy, x, weight, bias=None, initial_state=None, dfinal_state
         dbias = None if bias is None else weight.new_empty((dim,))
         line = (nseq, dim, width - 1)
         dinitial = None if initial_state is None else x.new_empty(line)
-        size = lib.causal_conv1d_bwd_workspace_size(T, dim, width) if workspace == "auto" else 0
+        size = lib.causal_conv1d_bwd_workspace_size(T, dim, width) if isinstance(workspace, str) else 0
         ws, ws_ptr, ws_bytes = _workspace(workspace, size, x, dev)
         st = lib.causal_conv1d_bwd(
             nseq, seqlen, _addr(cu_seqlens), dim, width, in_code,
@@ -1000,7 +996,7 @@ def ssm_pool_compact(pools, slot_idx, status=None, stream=None, workspace="auto"
     """Moves the live rows (those that slot_idx, int32 [nrows], names) to the
     front of every pool and rewrites slot_idx in place.  Returns their number,
     an int32 scalar tensor."""
-    if stream is None and workspace == "auto":
+    if stream is None and isinstance(workspace, str) and workspace == "auto":
         out = _marshal.pool_compact(pools, slot_idx, status)
         if _plain(out, "ssm_pool_compact"):
             return out[0]
@@ -1008,7 +1004,7 @@ def ssm_pool_compact(pools, slot_idx, status=None, stream=None, workspace="auto"
     with _scope(like, stream):
         dev, rows = like.get_device(), slot_idx.shape[0]
         live = slot_idx.new_empty(())
-        size = lib.ssm_pool_compact_workspace_size(slots, rows) if workspace == "auto" else 0
+        size = lib.ssm_pool_compact_workspace_size(slots, rows) if isinstance(workspace, str) else 0
         ws, ws_ptr, ws_bytes = _workspace(workspace, size, like, dev)
         st = lib.ssm_pool_compact(n, arr, slots, rows, _dev_like(slot_idx, "slot_idx", dev, _I32, (rows,)),
                                   live.data_ptr(), ws_ptr, ws_bytes, _dev_like(status, "status", dev, _I32),

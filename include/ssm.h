@@ -529,10 +529,9 @@ SSM_API int ssm_gated_rmsnorm(int rows, int dim, int group_size, int y_dtype, co
  *                in front of every 32nd token of a sequence.
  *   workspace / workspace_bytes  optional scratch of
  *                selective_scan_workspace_size(...) bytes, or NULL / 0.  With
- *                it, and without saved_states, a long token stream on few
- *                channels is cut into ranges that run concurrently (two
- *                launches); the states that cross a cut are joined in fp32, so
- *                results agree to rounding.  Calls that share a workspace
+ *                it, long sequences on few channels are cut into segments
+ *                that run concurrently (two launches); the states that cross a
+ *                cut are joined in fp32, so results agree to rounding.  Calls that share a workspace
  *                must not overlap on the GPU.
  */
 SSM_API int selective_scan_fwd(int nseq, int seqlen, const int32_t *cu_seqlens, int dim,

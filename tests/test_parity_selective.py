@@ -270,6 +270,25 @@ def test_scan_gradient_many_sequences_share_a_cta():
         close(t, want[k], mag[k], n, k)
 
 
+@pytest.mark.parametrize("lens,dim,N,G", [([1500, 0, 700, 1], 8, 16, 1), ([2000], 6, 5, 2), ([0, 1100, 0], 3, 64, 1),
+                                          ([640, 640], 16, 4, 1)])
+def test_scan_gradient_cut_into_segments(lens, dim, N, G):
+    """Long sequences on few channels: states and their gradients cross the cuts between segments."""
+    from hybrid_mamba_ssm_b200 import ssm
+    p = scan_case(23, lens, dim, N, G, "f32", "f32")
+    args, kw = operands(p, "f32", "f32")
+    rng = np.random.default_rng(24)
+    dy, dhT = rounder(F)(rng.standard_normal((sum(lens), dim))), rounder(F)(rng.standard_normal((len(lens), dim, N)))
+    y, hT, saved = ssm.selective_scan_fwd(*args, **kw, initial_state=dev(p["h0"]), cu_seqlens=cu_of(p), save_states=True)
+    g = ssm.selective_scan_bwd(dev(dy), *args, saved, **kw, dfinal_state=dev(dhT), cu_seqlens=cu_of(p), want_dinitial=True)
+    want, mag = ref.scan_grad(p, dy, dhT), ref.scan_grad(p, dy, dhT, magnitude=True)
+    n = ref.scan_rounding(p)
+    close(y, ref.scan(p)[0], ref.scan(p, magnitude=True)[0], n, "y")
+    for t, k in [(g.dx, "dx"), (g.ddt, "ddt"), (g.dA, "dA"), (g.dB, "dB"), (g.dC, "dC"), (g.dD, "dD"), (g.dz, "dz"),
+                 (g.ddt_bias, "dbias"), (g.dinitial_state, "dh0")]:
+        close(t, want[k], mag[k], n + (sum(lens) + dim if k in ("dA", "dB", "dC", "dD", "dbias") else 0), k)
+
+
 @pytest.mark.parametrize("dtype,dt", TYPES)
 @pytest.mark.parametrize("batch,dim,N,G", [(1, 64, 16, 1), (5, 130, 16, 2), (3, 33, 13, 1), (9, 7, 1, 1), (4, 12, 4, 3),
                                            (6, 20, 8, 1), (2, 24, 32, 2), (5, 10, 64, 1), (3, 6, 128, 1), (7, 5, 100, 1),
