@@ -18,9 +18,8 @@
 // window holds dpre, so din of token t is complete K-1 tokens later.  The
 // tile's first K-1 and last K-1 tokens depend on its neighbours: the walk
 // starts with the inputs of the K-1 tokens before the tile and runs K-1 tokens
-// past its end, recomputing their dpre (2 (K-1) of 128 tokens are read twice,
-// from L2).  A tile is 128 - (K-1) tokens, so that a walk inside one sequence
-// is a whole number of groups.  Weight and bias sums stay in registers over
+// past its end, recomputing their dpre (2 (K-1) tokens of a tile are read
+// twice, from L2).  Weight and bias sums stay in registers over
 // the tile and are added up over the tiles by a second launch, in a fixed
 // order.  Bound by HBM: x and dy read once, dx written once.
 #include "selective.cuh"
@@ -32,7 +31,12 @@ namespace {
 constexpr int kBwdThreads = 128;
 constexpr int kGroup = 8;
 
-constexpr int tile_tokens(int K) { return 128 - (K - 1); }
+// Tokens of a tile: a walk inside one sequence is `walk` tokens, K - 1 of them
+// behind the tile.  128, or 32 where that leaves fewer than two CTAs an SM (a
+// walk is a chain of its groups: 701 tokens of 1002 channels take 22 us in 24
+// CTAs of 128, 8 us in 88 of 32).
+__host__ __device__ __forceinline__ int tile_tokens(int walk, int K) { return walk - (K - 1); }
+inline int walk_tokens(long T, int dim) { return T * dim < 2L * 148 * 128 * (2 * kBwdThreads) ? 32 : 128; }
 
 // Raw values of channels c, c + 1 of a row (the second only where it exists).
 template <typename T, bool kPair>
@@ -59,13 +63,14 @@ __device__ __forceinline__ void store_two(T *row, int c, bool both, f32x2 v) {
 // kPair: dim is even, so two channels are one aligned access.
 template <typename T, int K, bool kPair>
 __global__ void __launch_bounds__(kBwdThreads, K <= 4 ? 4 : 3)
-conv1d_bwd_kernel(ConvBwdArgs a, int ctiles)
+conv1d_bwd_kernel(ConvBwdArgs a, int ctiles, int walk)
 {
     constexpr int H = K - 1;                  // history entries
     const int c = ((int)(blockIdx.x % ctiles) * kBwdThreads + threadIdx.x) * 2;
     const long tile = blockIdx.x / ctiles;
     const long total = a.cu_seqlens ? (long)a.seqlen : (long)a.nseq * a.seqlen;
-    const long t0 = tile * tile_tokens(K), t1 = min(t0 + tile_tokens(K), total);
+    const int len = tile_tokens(walk, K);
+    const long t0 = tile * len, t1 = min(t0 + len, total);
     if (c >= a.dim) return;
     const bool both = kPair || c + 1 < a.dim;
     const int c1 = both ? c + 1 : c;
@@ -242,44 +247,44 @@ __global__ void conv1d_bwd_empty_kernel(ConvBwdArgs a)
     for (long i = threadIdx.x; i < n; i += blockDim.x) store_out(out + i, in ? load_f32(in + s * n + i) : 0.f);
 }
 
-// dweight / dbias: sums of the tiles' parts.  32 channels x 32 tile lanes a
-// CTA; lane sums are added in a fixed tree, so the result does not depend on
-// the order in which CTAs ran.
-__global__ void __launch_bounds__(1024)
-conv1d_bwd_sum_kernel(ConvBwdArgs a, long tiles)
+// dweight / dbias: sums of the tiles' parts, 64 channels x 4 tile lanes a CTA.
+// Lane sums are added in a fixed order, so the result does not depend on the
+// order in which CTAs ran.
+__global__ void __launch_bounds__(256)
+conv1d_bwd_sum_kernel(ConvBwdArgs a, int tiles)
 {
-    __shared__ float red[32][33];
-    const int cx = threadIdx.x & 31, ty = threadIdx.x >> 5;
-    const int c = blockIdx.x * 32 + cx, k = blockIdx.y, K = a.width;
+    __shared__ float red[4][64];
+    const int cx = threadIdx.x & 63, ty = threadIdx.x >> 6;
+    const int c = blockIdx.x * 64 + cx, k = blockIdx.y, K = a.width;
     float v = 0.f;
-    if (c < a.dim)
-        for (long i = ty; i < tiles; i += 32) v += a.part[(i * (K + 1) + k) * a.dim + c];
+    if (c < a.dim) {
+        const float *p = a.part + (long)k * a.dim + c;
+#pragma unroll 8
+        for (int i = ty; i < tiles; i += 4) v += p[(long)i * (K + 1) * a.dim];
+    }
     red[ty][cx] = v;
     __syncthreads();
-    v = red[cx][ty];                            // tile lane cx of channel ty
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    const int co = blockIdx.x * 32 + ty;
-    if (cx == 0 && co < a.dim) {
-        if (k < K) a.dweight[(long)co * K + k] = v;
-        else if (a.dbias) a.dbias[co] = v;
-    }
+    if (ty || c >= a.dim) return;
+    v = (red[0][cx] + red[1][cx]) + (red[2][cx] + red[3][cx]);
+    if (k < K) a.dweight[(long)c * K + k] = v;
+    else if (a.dbias) a.dbias[c] = v;
 }
 
 template <typename T, int K>
 cudaError_t launch_k(const ConvBwdArgs &a, cudaStream_t stream)
 {
     const long total = a.cu_seqlens ? (long)a.seqlen : (long)a.nseq * a.seqlen;
-    const long tiles = (total + tile_tokens(K) - 1) / tile_tokens(K);
+    const int walk = walk_tokens(total, a.dim), len = tile_tokens(walk, K);
+    const long tiles = (total + len - 1) / len;
     if (tiles > 0) {
         const int ctiles = (a.dim + 2 * kBwdThreads - 1) / (2 * kBwdThreads);
         if (tiles * ctiles > 0x7fffffffL) return cudaErrorInvalidValue;
         const unsigned blocks = (unsigned)(tiles * ctiles);
-        if (a.dim % 2 == 0) conv1d_bwd_kernel<T, K, true><<<blocks, kBwdThreads, 0, stream>>>(a, ctiles);
-        else conv1d_bwd_kernel<T, K, false><<<blocks, kBwdThreads, 0, stream>>>(a, ctiles);
+        if (a.dim % 2 == 0) conv1d_bwd_kernel<T, K, true><<<blocks, kBwdThreads, 0, stream>>>(a, ctiles, walk);
+        else conv1d_bwd_kernel<T, K, false><<<blocks, kBwdThreads, 0, stream>>>(a, ctiles, walk);
     }
     if (a.dinitial && K > 1) conv1d_bwd_empty_kernel<T><<<(unsigned)a.nseq, 256, 0, stream>>>(a);
-    conv1d_bwd_sum_kernel<<<dim3((unsigned)((a.dim + 31) / 32), (unsigned)(K + 1)), 1024, 0, stream>>>(a, tiles);
+    conv1d_bwd_sum_kernel<<<dim3((unsigned)((a.dim + 63) / 64), (unsigned)(K + 1)), 256, 0, stream>>>(a, (int)tiles);
     return cudaGetLastError();
 }
 
@@ -302,7 +307,7 @@ cudaError_t launch_t(const ConvBwdArgs &a, cudaStream_t stream)
 
 size_t conv1d_bwd_workspace(long T, int dim, int width)
 {
-    const long n = tile_tokens(width);
+    const long n = tile_tokens(walk_tokens(T, dim), width);
     return (size_t)((T + n - 1) / n) * (width + 1) * dim * sizeof(float);
 }
 

@@ -45,6 +45,16 @@ __device__ __forceinline__ f32x2 ex2_pair(f32x2 a) {
     return pack2(ex2_approx(lo2(a)), ex2_approx(hi2(a)));
 }
 
+// Decays 2^(v A) (A in units of log2 e).  ex2.approx is 2e-8 of its value low
+// on average between 2^-0.5 and 2^-0.003 (measured here), which a long memory
+// adds up: a state that lasts 300 tokens would come out 6e-6 small.  kEx2Bias in
+// the exponent takes the average out, at no cost (an fma for a product); it
+// rounds away where the decay is exactly 1.
+constexpr float kEx2Bias = 2.9e-8f;
+__device__ __forceinline__ f32x2 decay2(f32x2 v, f32x2 A) {
+    return ex2_pair(fma2(v, A, pack2(kEx2Bias, kEx2Bias)));
+}
+
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 

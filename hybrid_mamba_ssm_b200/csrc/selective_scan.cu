@@ -38,6 +38,8 @@ struct ScanShape {
     static constexpr int E = (KT + RS - 1) / RS;                 // staged pairs per thread
     static constexpr int EB = (KT * NP + kThreads - 1) / kThreads;
     static constexpr int YP = L < 4 ? L : 4;                     // partial sums over n left to the output step
+    // two buffers of v and v x, of B and C, and of the partial sums of y
+    static constexpr size_t bytes(bool out) { return sizeof(float) * (4 * KT * CT + 4 * KT * NP + (out ? 2 * KT * CT * YP : 0)); }
     static_assert(KT % TG == 0 && CT % 2 == 0, "");
 };
 
@@ -104,10 +106,11 @@ selective_scan_kernel(SelScanArgs a)
     constexpr int P = R / 2, YP = S::YP;
     constexpr bool kOut = kMode != kRangeState;
     // two buffers each: a tile is staged while the one before is still read
-    __shared__ __align__(16) float2 s_vu[2][KT * CT];            // step size, step size times x
-    __shared__ __align__(16) float s_B[2][KT * NP];
-    __shared__ __align__(16) float s_C[2][kOut ? KT * NP : 4];
-    __shared__ __align__(16) float s_y[2][kOut ? KT * CT * YP : 4];
+    extern __shared__ __align__(16) float smem[];
+    auto s_vu = reinterpret_cast<float2 (*)[KT * CT]>(smem);     // step size, step size times x
+    auto s_B = reinterpret_cast<float (*)[KT * NP]>(smem + 4 * KT * CT);
+    auto s_C = reinterpret_cast<float (*)[KT * NP]>(smem + 4 * KT * CT + 2 * KT * NP);
+    auto s_y = reinterpret_cast<float (*)[KT * CT * YP]>(smem + 4 * KT * CT + 4 * KT * NP);
 
     const int tid = threadIdx.x, lane = tid & 31;
     const int gdim = a.dim / a.ngroups, gtiles = (gdim + CT - 1) / CT, tiles = gtiles * a.ngroups;
@@ -140,33 +143,44 @@ selective_scan_kernel(SelScanArgs a)
     // Raw values of the next tile; x and z of the one whose output is due.
     uint32_t xr[E][2], vr[E][2], zr[E][2], Br[EB], Cr[EB], xc[E][2], zc[E][2];
 
-    // Offsets of this thread's staged values from the tile's first row: 32 bits
-    // (strides are at most 2^24), so that an address is a uniform base plus one.
-    const int xs = (int)a.x_stride, vs = (int)a.dt_stride, Bs = (int)a.B_stride, Cs = (int)a.C_stride, zs = (int)a.z_stride;
-    const int x0 = st * xs + sc, v0 = st * vs + sc, z0 = st * zs + sc, y0 = st * a.dim + sc;
+    // Pointers to this thread's values of the tile to fetch, moved on tile by
+    // tile (the address arithmetic of the loads was a quarter of all
+    // instructions when it started from the operands' bases).
     const bool whole_rows = a.pairs && cend - c0 == CT && N == NP;   // no channel or state of the tile is padding
+    constexpr int BR = NP <= kThreads ? kThreads / NP : 1;           // tokens per staging step of B and C
+    const int bn = NP <= kThreads ? tid % NP : tid, bk = NP <= kThreads ? tid / NP : 0;
+    const TIn *px, *pz, *pB, *pC;
+    const TDt *pv;
+    auto seek = [&](long t) {
+        px = static_cast<const TIn *>(a.x) + (t + st) * a.x_stride + ds;
+        pv = static_cast<const TDt *>(a.dt) + (t + st) * a.dt_stride + ds;
+        pz = static_cast<const TIn *>(a.z) + (t + st) * a.z_stride + ds;
+        pB = static_cast<const TIn *>(a.B) + (t + bk) * a.B_stride + g * N + bn;
+        pC = static_cast<const TIn *>(a.C) + (t + bk) * a.C_stride + g * N + bn;
+    };
+    // Strides are at most 2^24 and a tile has at most 32 tokens: 32-bit offsets within it.
+    const int xs = (int)a.x_stride, vs = (int)a.dt_stride, Bs = (int)a.B_stride, Cs = (int)a.C_stride, zs = (int)a.z_stride;
 
-    // Raw values of n tokens from t on, zero behind them.
-    auto fetch = [&](long t, int n) {
-        const TIn *xt = static_cast<const TIn *>(a.x) + t * xs + c0;
-        const TIn *zt = static_cast<const TIn *>(a.z) + t * zs + c0;
-        const TDt *vt = static_cast<const TDt *>(a.dt) + t * vs + c0;
-        const TIn *Bt = static_cast<const TIn *>(a.B) + t * Bs + g * N;
-        const TIn *Ct = static_cast<const TIn *>(a.C) + t * Cs + g * N;
+    // Raw values of the next n tokens, zero behind them.
+    auto fetch = [&](int n) {
         if (n == KT && whole_rows) {
 #pragma unroll
             for (int i = 0; i < E; ++i) {
                 if (KT % RS && st + i * RS >= KT) break;
-                pair_load(xt, x0 + i * RS * xs, xr[i]);
-                pair_load(vt, v0 + i * RS * vs, vr[i]);
-                if (kOut && a.z) pair_load(zt, z0 + i * RS * zs, zr[i]);
+                pair_load(px, i * RS * xs, xr[i]);
+                pair_load(pv, i * RS * vs, vr[i]);
+                if (kOut && a.z) pair_load(pz, i * RS * zs, zr[i]);
             }
 #pragma unroll
             for (int i = 0; i < EB; ++i) {
-                const int e = tid + i * kThreads;
-                if (KT * NP % kThreads && e >= KT * NP) break;
-                Br[i] = raw_load<TIn>(Bt, e / NP * Bs + e % NP);
-                if (kOut) Cr[i] = raw_load<TIn>(Ct, e / NP * Cs + e % NP);
+                if (NP <= kThreads) {
+                    if (KT % BR && bk + i * BR >= KT) break;
+                    Br[i] = raw_load<TIn>(pB, i * BR * Bs);
+                    if (kOut) Cr[i] = raw_load<TIn>(pC, i * BR * Cs);
+                } else {                       // a row takes two steps
+                    Br[i] = raw_load<TIn>(pB, i / 2 * Bs + i % 2 * kThreads);
+                    if (kOut) Cr[i] = raw_load<TIn>(pC, i / 2 * Cs + i % 2 * kThreads);
+                }
             }
         } else {
 #pragma unroll
@@ -175,19 +189,25 @@ selective_scan_kernel(SelScanArgs a)
 #pragma unroll
                 for (int q = 0; q < 2; ++q) {
                     const bool ok = in && (q ? slive1 : slive0);
-                    xr[i][q] = ok ? raw_load<TIn>(xt, x0 + i * RS * xs + q) : 0u;
-                    vr[i][q] = ok ? raw_load<TDt>(vt, v0 + i * RS * vs + q) : 0u;
-                    if (kOut) zr[i][q] = ok && a.z ? raw_load<TIn>(zt, z0 + i * RS * zs + q) : 0u;
+                    xr[i][q] = ok ? raw_load<TIn>(px, i * RS * xs + q) : 0u;
+                    vr[i][q] = ok ? raw_load<TDt>(pv, i * RS * vs + q) : 0u;
+                    if (kOut) zr[i][q] = ok && a.z ? raw_load<TIn>(pz, i * RS * zs + q) : 0u;
                 }
             }
 #pragma unroll
             for (int i = 0; i < EB; ++i) {
-                const int e = tid + i * kThreads;
-                const bool ok = e % NP < N && e / NP < n;
-                Br[i] = ok ? raw_load<TIn>(Bt, e / NP * Bs + e % NP) : 0u;
-                if (kOut) Cr[i] = ok ? raw_load<TIn>(Ct, e / NP * Cs + e % NP) : 0u;
+                const int k = NP <= kThreads ? bk + i * BR : i / 2, add = NP <= kThreads ? 0 : i % 2 * kThreads;
+                const int from = NP <= kThreads ? i * BR : i / 2;
+                const bool ok = bn + add < N && k < n;
+                Br[i] = ok ? raw_load<TIn>(pB, from * Bs + add) : 0u;
+                if (kOut) Cr[i] = ok ? raw_load<TIn>(pC, from * Cs + add) : 0u;
             }
         }
+        px += (long)n * xs;
+        pv += (long)n * vs;
+        pz += (long)n * zs;
+        pB += (long)n * Bs;
+        pC += (long)n * Cs;
     };
     // Step sizes, B and C of the fetched tile of n tokens into buffer b.
     auto stage = [&](int n, int b) {
@@ -196,7 +216,7 @@ selective_scan_kernel(SelScanArgs a)
             const int k = st + i * RS;
             if (KT % RS && k >= KT) break;
             f32x2 v = dt_value2(a.dtp, pair_value<TDt>(vr[i]), bias);
-            if (k >= n) v = pack2(0.f, 0.f);       // tokens behind the tile leave the state as it is
+            if (n < KT && k >= n) v = pack2(0.f, 0.f);   // tokens behind the tile leave the state as it is
             const f32x2 u = mul2(v, pair_value<TIn>(xr[i]));
             *reinterpret_cast<float4 *>(&s_vu[b][k * CT + sc]) = make_float4(lo2(v), lo2(u), hi2(v), hi2(u));
         }
@@ -208,9 +228,8 @@ selective_scan_kernel(SelScanArgs a)
             if (kOut) s_C[b][e] = raw_value<TIn>(Cr[i]);
         }
     };
-    // y of a tile of n tokens from t on, from the partial sums of buffer b.
-    auto output = [&](long t, int n, int b) {
-        const long yt = t * a.dim + c0;
+    // y of a tile of n tokens, from the partial sums of buffer b; this thread's first is element `first`.
+    auto output = [&](long first, int n, int b) {
 #pragma unroll
         for (int i = 0; i < E; ++i) {
             const int k = st + i * RS;
@@ -228,9 +247,9 @@ selective_scan_kernel(SelScanArgs a)
             }
             f32x2 y = fma2(skip, pair_value<TIn>(xc[i]), pack2(f[0], f[1]));
             if (a.z) y = mul2(y, silu2(pair_value<TIn>(zc[i])));
-            const int o = y0 + i * RS * a.dim;
+            const int o = i * RS * a.dim;
             if (a.y_bf16) {
-                __nv_bfloat16 *yp = static_cast<__nv_bfloat16 *>(a.y) + yt + o;
+                __nv_bfloat16 *yp = static_cast<__nv_bfloat16 *>(a.y) + first + o;
                 if (slive1 && gdim % 2 == 0) {      // the even channel of a pair is even in y too
                     *reinterpret_cast<__nv_bfloat162 *>(yp) = __floats2bfloat162_rn(lo2(y), hi2(y));
                 } else {
@@ -238,7 +257,7 @@ selective_scan_kernel(SelScanArgs a)
                     if (slive1) store_out(yp + 1, hi2(y));
                 }
             } else {
-                float *yp = static_cast<float *>(a.y) + yt + o;
+                float *yp = static_cast<float *>(a.y) + first + o;
                 store_out(yp, lo2(y));
                 if (slive1) store_out(yp + 1, hi2(y));
             }
@@ -250,12 +269,15 @@ selective_scan_kernel(SelScanArgs a)
     auto run = [&](long t, long te, long lo, long save0) {
         int rel = (int)(t - lo), left = (int)(te - t), before = 0, b = 0;
         int n = min(left, KT - rel % KT);          // tiles end on multiples of KT of the sequence
-        fetch(t, n);
+        seek(t);
+        fetch(n);
+        long out = (t + st) * a.dim + ds;          // y of the tile before, at this thread's first token
         while (left > 0) {
             stage(n, b);
             __syncthreads();
             if (kOut) {
-                if (before) output(t - before, before, b ^ 1);
+                if (before) output(out, before, b ^ 1);
+                out += (long)before * a.dim;
 #pragma unroll
                 for (int i = 0; i < E; ++i)
 #pragma unroll
@@ -265,7 +287,7 @@ selective_scan_kernel(SelScanArgs a)
                     }
             }
             const int n2 = min(left - n, KT);
-            if (n2 > 0) fetch(t + n, n2);
+            if (n2 > 0) fetch(n2);
             if (kOut && a.saved && rel % kSavedEvery == 0) {
 #pragma unroll
                 for (int q = 0; q < Q; ++q)
@@ -286,7 +308,7 @@ selective_scan_kernel(SelScanArgs a)
                         f32x2 acc;
 #pragma unroll
                         for (int p = 0; p < P; ++p) {
-                            h[q][p] = fma2(ex2_pair(mul2(vv, A[q][p])), h[q][p], mul2(uu, B[p]));
+                            h[q][p] = fma2(decay2(vv, A[q][p]), h[q][p], mul2(uu, B[p]));
                             if (kOut) acc = p ? fma2(h[q][p], C[p], acc) : mul2(h[q][p], C[p]);
                         }
                         if (kOut) {
@@ -311,7 +333,6 @@ selective_scan_kernel(SelScanArgs a)
                     }
                 }
             }
-            t += n;
             rel += n;
             left -= n;
             before = n;
@@ -319,7 +340,7 @@ selective_scan_kernel(SelScanArgs a)
             b ^= 1;
         }
         __syncthreads();
-        if (kOut) output(t - before, before, b ^ 1);
+        if (kOut) output(out, before, b ^ 1);
         __syncthreads();                           // the next sequence stages into either buffer
     };
 
@@ -377,7 +398,7 @@ selective_scan_kernel(SelScanArgs a)
                 const float v = live(q) ? a.range_dt[(w.base + i) * a.dim + d0 + q * CS] : 0.f;
 #pragma unroll
                 for (int p = 0; p < P; ++p)
-                    h[q][p] = fma2(ex2_pair(mul2(pack2(v, v), A[q][p])), h[q][p], e[q][p]);
+                    h[q][p] = fma2(decay2(pack2(v, v), A[q][p]), h[q][p], e[q][p]);
             }
         }
     } else if (kMode == kRangeOut && w.e < w.hi) {
@@ -390,6 +411,17 @@ selective_scan_kernel(SelScanArgs a)
     if (w.e == w.hi && a.final && (w.lo < w.hi || a.final != a.initial || !init)) store_all(a.final, row);
 }
 
+template <typename TIn, typename TDt, int R, int L, int Q, int kMode>
+cudaError_t launch_mode(const SelScanArgs &a, unsigned blocks, cudaStream_t stream)
+{
+    constexpr size_t bytes = ScanShape<R, L, Q>::bytes(kMode != kRangeState);
+    if (bytes > 48 * 1024)
+        if (const cudaError_t e = cudaFuncSetAttribute(selective_scan_kernel<TIn, TDt, R, L, Q, kMode>,
+                                                       cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes)) return e;
+    selective_scan_kernel<TIn, TDt, R, L, Q, kMode><<<blocks, kThreads, bytes, stream>>>(a);
+    return cudaGetLastError();
+}
+
 template <typename TIn, typename TDt, int R, int L, int Q>
 cudaError_t launch_shape(const SelScanArgs &a, cudaStream_t stream)
 {
@@ -397,13 +429,9 @@ cudaError_t launch_shape(const SelScanArgs &a, cudaStream_t stream)
     const long long tiles = (long long)((gdim + CT - 1) / CT) * a.ngroups;
     if (tiles * a.units > 0x7fffffffLL) return cudaErrorInvalidValue;
     const unsigned blocks = (unsigned)(tiles * a.units);
-    if (!a.span) {
-        selective_scan_kernel<TIn, TDt, R, L, Q, kWhole><<<blocks, kThreads, 0, stream>>>(a);
-        return cudaGetLastError();
-    }
-    selective_scan_kernel<TIn, TDt, R, L, Q, kRangeState><<<blocks, kThreads, 0, stream>>>(a);
-    selective_scan_kernel<TIn, TDt, R, L, Q, kRangeOut><<<blocks, kThreads, 0, stream>>>(a);
-    return cudaGetLastError();
+    if (!a.span) return launch_mode<TIn, TDt, R, L, Q, kWhole>(a, blocks, stream);
+    if (const cudaError_t e = launch_mode<TIn, TDt, R, L, Q, kRangeState>(a, blocks, stream)) return e;
+    return launch_mode<TIn, TDt, R, L, Q, kRangeOut>(a, blocks, stream);
 }
 
 template <typename TIn, typename TDt>

@@ -185,7 +185,7 @@ selective_scan_bwd_kernel(SelScanBwdArgs b, int ctas)
                     load_row<R>(a.range_state + ((w.base + m) * a.dim + d) * N, j, N, own);
                     const float v = a.range_dt[(w.base + m) * a.dim + d];
 #pragma unroll
-                    for (int p = 0; p < P; ++p) G[q][p] = fma2(ex2_pair(mul2(pack2(v, v), A[q][p])), G[q][p], own[p]);
+                    for (int p = 0; p < P; ++p) G[q][p] = fma2(decay2(pack2(v, v), A[q][p]), G[q][p], own[p]);
                 }
             }
         }
@@ -302,7 +302,7 @@ selective_scan_bwd_kernel(SelScanBwdArgs b, int ctas)
                         vsum[q] += v[q];
 #pragma unroll
                         for (int p = 0; p < P; ++p)
-                            G[q][p] = mul2(ex2_pair(mul2(pack2(v[q], v[q]), A[q][p])), fma2(pack2(g[q], g[q]), C[p], G[q][p]));
+                            G[q][p] = mul2(decay2(pack2(v[q], v[q]), A[q][p]), fma2(pack2(g[q], g[q]), C[p], G[q][p]));
                     }
                 }
                 __syncthreads();
@@ -329,7 +329,7 @@ selective_scan_bwd_kernel(SelScanBwdArgs b, int ctas)
                     for (int q = 0; q < CS; ++q)
 #pragma unroll
                         for (int p = 0; p < P; ++p)
-                            h[q][p] = fma2(ex2_pair(mul2(pack2(v[q], v[q]), A[q][p])), h[q][p], mul2(pack2(u[q], u[q]), B[p]));
+                            h[q][p] = fma2(decay2(pack2(v[q], v[q]), A[q][p]), h[q][p], mul2(pack2(u[q], u[q]), B[p]));
                 }
             }
 
@@ -388,7 +388,7 @@ selective_scan_bwd_kernel(SelScanBwdArgs b, int ctas)
                     for (int k = 0; k < kSub; ++k)
 #pragma unroll
                         for (int p = 0; p < P; ++p) {
-                            aa[k][p] = ex2_pair(mul2(pack2(v[k][q], v[k][q]), A[q][p]));
+                            aa[k][p] = decay2(pack2(v[k][q], v[k][q]), A[q][p]);
                             hh[k + 1][p] = fma2(aa[k][p], hh[k][p], mul2(pack2(u[k][q], u[k][q]), B[k][p]));
                         }
 #pragma unroll

@@ -145,6 +145,24 @@ def test_scan_cut_into_ranges(lens, dim, N, G, inplace):
     close(hT, wT, mT, ref.scan_rounding(p), "final state")
 
 
+def test_a_step_of_zero_leaves_the_state_bit_for_bit():
+    """exp(0 A) is exactly 1 in every kernel, whatever is added to its argument."""
+    from hybrid_mamba_ssm_b200 import ssm
+    p = scan_case(14, [40], 64, 16, softplus=False, bias=False, D=False, gate=False)
+    (x, d, A, B, C), _ = operands(p, "bf16", "f32")
+    h0 = dev(p["h0"])
+    zero = torch.zeros_like(d)
+    y, hT, saved = ssm.selective_scan_fwd(x, zero, A, B, C, initial_state=h0, cu_seqlens=cu_of(p), save_states=True)
+    assert torch.equal(hT, h0)
+    dhT = torch.randn_like(h0)
+    g = ssm.selective_scan_bwd(torch.zeros_like(x), x, zero, A, B, C, saved, dfinal_state=dhT, cu_seqlens=cu_of(p),
+                               want_dinitial=True)
+    assert torch.equal(g.dinitial_state, dhT)
+    state = h0.clone()
+    ssm.selective_state_update(state, x[:1], zero[:1], A, B[:1], C[:1])
+    assert torch.equal(state, h0)
+
+
 def test_scan_slots_in_place():
     from hybrid_mamba_ssm_b200 import ssm
     lens, dim, N = [20, 0, 7, 0], 64, 16
