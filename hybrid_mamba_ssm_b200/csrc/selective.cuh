@@ -208,6 +208,41 @@ __device__ __forceinline__ void prefetch_l2(const void *p) {
     asm volatile("prefetch.global.L2 [%0];" :: "l"(p));
 }
 
+// Two adjacent values as loaded.  kPacked: they are one aligned access, so a
+// bf16 pair is one register.
+template <typename T, bool kPacked>
+struct RawPair {
+    uint32_t r[sizeof(T) == 2 && kPacked ? 1 : 2];
+    __device__ __forceinline__ void zero() {
+#pragma unroll
+        for (int i = 0; i < (int)(sizeof(r) / 4); ++i) r[i] = 0u;
+    }
+    // values p[i], p[i + 1]; p + i is aligned to both
+    __device__ __forceinline__ void load(const T *p, int i) {
+        static_assert(kPacked, "");
+        if constexpr (sizeof(T) == 2) {
+            r[0] = *reinterpret_cast<const uint32_t *>(p + i);
+        } else {
+            const uint2 q = *reinterpret_cast<const uint2 *>(p + i);
+            r[0] = q.x;
+            r[1] = q.y;
+        }
+    }
+    // one by one; ok1 without ok0 does not happen
+    __device__ __forceinline__ void load(const T *p, int i, bool ok0, bool ok1) {
+        if constexpr (sizeof(r) == 4) {
+            r[0] = ok0 ? (uint32_t)raw_load<T>(p, i) | (ok1 ? (uint32_t)raw_load<T>(p, i + 1) << 16 : 0u) : 0u;
+        } else {
+            r[0] = ok0 ? raw_load<T>(p, i) : 0u;
+            r[1] = ok1 ? raw_load<T>(p, i + 1) : 0u;
+        }
+    }
+    __device__ __forceinline__ f32x2 value() const {
+        if constexpr (sizeof(r) == 4) return pack2(__uint_as_float(r[0] << 16), __uint_as_float(r[0] & 0xffff0000u));
+        else return pack2(raw_value<T>(r[0]), raw_value<T>(r[1]));
+    }
+};
+
 // Two adjacent values.  pair_load wants an address aligned to both; either way
 // the registers hold what pair_value takes: a bf16 pair is one register, or
 // two with a value in the low half of each.

@@ -17,6 +17,8 @@
 // exactly once, then read by the channel's L lanes, while the next tile's
 // global loads are in flight.  The sums over n of a few tokens are exchanged
 // together (reduce_lanes), so they cost about one shuffle per token and lane.
+#include <type_traits>
+
 #include "selective.cuh"
 
 namespace ssm {
@@ -97,7 +99,7 @@ enum { kWhole = 0, kRangeState = 1, kRangeOut = 2 };
 // enters it by exp(A sum v).  It also copies the initial state.  The second
 // folds the segments before its own and runs its tokens from the state that
 // enters.
-template <typename TIn, typename TDt, int R, int L, int Q, int kMode>
+template <typename TIn, typename TDt, int R, int L, int Q, int kMode, bool kPacked>
 __global__ void __launch_bounds__(kThreads, kMinBlocks<R, Q>)
 selective_scan_kernel(SelScanArgs a)
 {
@@ -141,12 +143,14 @@ selective_scan_kernel(SelScanArgs a)
         for (int p = 0; p < P; ++p) A[q][p] = mul2(A[q][p], pack2(kLog2e, kLog2e));
     }
     // Raw values of the next tile; x and z of the one whose output is due.
-    uint32_t xr[E][2], vr[E][2], zr[E][2], Br[EB], Cr[EB], xc[E][2], zc[E][2];
+    RawPair<TIn, kPacked> xr[E], zr[E], xc[E], zc[E];
+    RawPair<TDt, kPacked> vr[E];
+    uint32_t Br[EB], Cr[EB];
 
     // Pointers to this thread's values of the tile to fetch, moved on tile by
     // tile (the address arithmetic of the loads was a quarter of all
     // instructions when it started from the operands' bases).
-    const bool whole_rows = a.pairs && cend - c0 == CT && N == NP;   // no channel or state of the tile is padding
+    const bool whole_rows = kPacked && cend - c0 == CT && N == NP;   // no channel or state of the tile is padding
     constexpr int BR = NP <= kThreads ? kThreads / NP : 1;           // tokens per staging step of B and C
     const int bn = NP <= kThreads ? tid % NP : tid, bk = NP <= kThreads ? tid / NP : 0;
     const TIn *px, *pz, *pB, *pC;
@@ -167,9 +171,11 @@ selective_scan_kernel(SelScanArgs a)
 #pragma unroll
             for (int i = 0; i < E; ++i) {
                 if (KT % RS && st + i * RS >= KT) break;
-                pair_load(px, i * RS * xs, xr[i]);
-                pair_load(pv, i * RS * vs, vr[i]);
-                if (kOut && a.z) pair_load(pz, i * RS * zs, zr[i]);
+                if constexpr (kPacked) {
+                    xr[i].load(px, i * RS * xs);
+                    vr[i].load(pv, i * RS * vs);
+                    if (kOut && a.z) zr[i].load(pz, i * RS * zs);
+                }
             }
 #pragma unroll
             for (int i = 0; i < EB; ++i) {
@@ -185,14 +191,10 @@ selective_scan_kernel(SelScanArgs a)
         } else {
 #pragma unroll
             for (int i = 0; i < E; ++i) {
-                const bool in = st + i * RS < n;
-#pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    const bool ok = in && (q ? slive1 : slive0);
-                    xr[i][q] = ok ? raw_load<TIn>(px, i * RS * xs + q) : 0u;
-                    vr[i][q] = ok ? raw_load<TDt>(pv, i * RS * vs + q) : 0u;
-                    if (kOut) zr[i][q] = ok && a.z ? raw_load<TIn>(pz, i * RS * zs + q) : 0u;
-                }
+                const bool ok0 = slive0 && st + i * RS < n, ok1 = slive1 && ok0;
+                xr[i].load(px, i * RS * xs, ok0, ok1);
+                vr[i].load(pv, i * RS * vs, ok0, ok1);
+                if (kOut) zr[i].load(pz, i * RS * zs, ok0 && a.z, ok1 && a.z);
             }
 #pragma unroll
             for (int i = 0; i < EB; ++i) {
@@ -215,9 +217,9 @@ selective_scan_kernel(SelScanArgs a)
         for (int i = 0; i < E; ++i) {
             const int k = st + i * RS;
             if (KT % RS && k >= KT) break;
-            f32x2 v = dt_value2(a.dtp, pair_value<TDt>(vr[i]), bias);
+            f32x2 v = dt_value2(a.dtp, vr[i].value(), bias);
             if (n < KT && k >= n) v = pack2(0.f, 0.f);   // tokens behind the tile leave the state as it is
-            const f32x2 u = mul2(v, pair_value<TIn>(xr[i]));
+            const f32x2 u = mul2(v, xr[i].value());
             *reinterpret_cast<float4 *>(&s_vu[b][k * CT + sc]) = make_float4(lo2(v), lo2(u), hi2(v), hi2(u));
         }
 #pragma unroll
@@ -245,8 +247,8 @@ selective_scan_kernel(SelScanArgs a)
                     f[q] = sum2(YP == 4 ? add2(part[0], part[YP / 2 - 1]) : part[0]);
                 }
             }
-            f32x2 y = fma2(skip, pair_value<TIn>(xc[i]), pack2(f[0], f[1]));
-            if (a.z) y = mul2(y, silu2(pair_value<TIn>(zc[i])));
+            f32x2 y = fma2(skip, xc[i].value(), pack2(f[0], f[1]));
+            if (a.z) y = mul2(y, silu2(zc[i].value()));
             const int o = i * RS * a.dim;
             if (a.y_bf16) {
                 __nv_bfloat16 *yp = static_cast<__nv_bfloat16 *>(a.y) + first + o;
@@ -279,12 +281,10 @@ selective_scan_kernel(SelScanArgs a)
                 if (before) output(out, before, b ^ 1);
                 out += (long)before * a.dim;
 #pragma unroll
-                for (int i = 0; i < E; ++i)
-#pragma unroll
-                    for (int q = 0; q < 2; ++q) {
-                        xc[i][q] = xr[i][q];
-                        zc[i][q] = zr[i][q];
-                    }
+                for (int i = 0; i < E; ++i) {
+                    xc[i] = xr[i];
+                    zc[i] = zr[i];
+                }
             }
             const int n2 = min(left - n, KT);
             if (n2 > 0) fetch(n2);
@@ -411,14 +411,14 @@ selective_scan_kernel(SelScanArgs a)
     if (w.e == w.hi && a.final && (w.lo < w.hi || a.final != a.initial || !init)) store_all(a.final, row);
 }
 
-template <typename TIn, typename TDt, int R, int L, int Q, int kMode>
+template <typename TIn, typename TDt, int R, int L, int Q, int kMode, bool kPacked>
 cudaError_t launch_mode(const SelScanArgs &a, unsigned blocks, cudaStream_t stream)
 {
     constexpr size_t bytes = ScanShape<R, L, Q>::bytes(kMode != kRangeState);
     if (bytes > 48 * 1024)
-        if (const cudaError_t e = cudaFuncSetAttribute(selective_scan_kernel<TIn, TDt, R, L, Q, kMode>,
+        if (const cudaError_t e = cudaFuncSetAttribute(selective_scan_kernel<TIn, TDt, R, L, Q, kMode, kPacked>,
                                                        cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes)) return e;
-    selective_scan_kernel<TIn, TDt, R, L, Q, kMode><<<blocks, kThreads, bytes, stream>>>(a);
+    selective_scan_kernel<TIn, TDt, R, L, Q, kMode, kPacked><<<blocks, kThreads, bytes, stream>>>(a);
     return cudaGetLastError();
 }
 
@@ -429,9 +429,13 @@ cudaError_t launch_shape(const SelScanArgs &a, cudaStream_t stream)
     const long long tiles = (long long)((gdim + CT - 1) / CT) * a.ngroups;
     if (tiles * a.units > 0x7fffffffLL) return cudaErrorInvalidValue;
     const unsigned blocks = (unsigned)(tiles * a.units);
-    if (!a.span) return launch_mode<TIn, TDt, R, L, Q, kWhole>(a, blocks, stream);
-    if (const cudaError_t e = launch_mode<TIn, TDt, R, L, Q, kRangeState>(a, blocks, stream)) return e;
-    return launch_mode<TIn, TDt, R, L, Q, kRangeOut>(a, blocks, stream);
+    auto run = [&](auto packed) -> cudaError_t {
+        constexpr bool kPacked = decltype(packed)::value;
+        if (!a.span) return launch_mode<TIn, TDt, R, L, Q, kWhole, kPacked>(a, blocks, stream);
+        if (const cudaError_t e = launch_mode<TIn, TDt, R, L, Q, kRangeState, kPacked>(a, blocks, stream)) return e;
+        return launch_mode<TIn, TDt, R, L, Q, kRangeOut, kPacked>(a, blocks, stream);
+    };
+    return a.pairs ? run(std::true_type{}) : run(std::false_type{});
 }
 
 template <typename TIn, typename TDt>

@@ -109,7 +109,7 @@ constexpr int kCtasPerSm = R > 4 ? 1 : CS == 2 ? 3 : 4;
 // the segment's own tokens give it (the last one of a sequence: from the final
 // state's gradient), and the sum of its step sizes; the main pass folds the
 // segments behind its own.
-template <typename TIn, typename TDt, int R, int L, int CS, bool kCarry>
+template <typename TIn, typename TDt, int R, int L, int CS, bool kCarry, bool kPacked>
 __global__ void __launch_bounds__(kBwdThreads, kCtasPerSm<R, CS>)
 selective_scan_bwd_kernel(SelScanBwdArgs b, int ctas)
 {
@@ -142,10 +142,10 @@ selective_scan_bwd_kernel(SelScanBwdArgs b, int ctas)
     const int xs = (int)a.x_stride, vs = (int)a.dt_stride, ys = (int)b.dy_stride, zs = (int)a.z_stride;
     const int Bs = (int)a.B_stride, Cs = (int)a.C_stride;
     // this lane's own two channels as one access (loads, and stores into rows of dim values)
-    const bool pair_in = CS == 2 && a.pairs && dc + 1 < cend, pair_out = CS == 2 && gdim % 2 == 0 && dc + 1 < cend;
+    const bool pair_in = CS == 2 && kPacked && dc + 1 < cend, pair_out = CS == 2 && gdim % 2 == 0 && dc + 1 < cend;
     const f32x2 own_bias = pack2(a.dtp.bias && dc < cend ? a.dtp.bias[dc] : 0.f, a.dtp.bias && CS == 2 && dc + 1 < cend ? a.dtp.bias[dc + 1] : 0.f);
     const f32x2 own_skip = pack2(a.D && dc < cend ? a.D[dc] : 0.f, a.D && CS == 2 && dc + 1 < cend ? a.D[dc + 1] : 0.f);
-    const bool whole_rows = a.pairs && cend - c0 == CB && N == NP;
+    const bool whole_rows = kPacked && cend - c0 == CB && N == NP;
 
     f32x2 A[CS][P], G[CS][P], dA[CS][P];
     f32x2 sum_D = pack2(0.f, 0.f), sum_bias = sum_D;  // of this lane's channel(s)
@@ -216,34 +216,34 @@ selective_scan_bwd_kernel(SelScanBwdArgs b, int ctas)
             constexpr int kStep = KC / RS < 4 ? (KC / RS < 1 ? 1 : KC / RS) : 4;   // tokens whose loads are in flight together
 #pragma unroll 1
             for (int k0 = st; k0 < KC; k0 += RS * kStep) {
-                uint32_t rv[kStep][2], rx[kStep][2], rg[kStep][2], rz[kStep][2];
+                RawPair<TDt, kPacked> rv[kStep];
+                RawPair<TIn, kPacked> rx[kStep], rg[kStep], rz[kStep];
 #pragma unroll
                 for (int i = 0; i < kStep; ++i) {
                     const int k = k0 + i * RS;
                     if (full) {
-                        pair_load(vt, k * vs + sc, rv[i]);
-                        pair_load(xt, k * xs + sc, rx[i]);
-                        pair_load(yt, k * ys + sc, rg[i]);
-                        if (a.z) pair_load(zt, k * zs + sc, rz[i]);
-                    } else {
-#pragma unroll
-                        for (int w = 0; w < 2; ++w) {
-                            const bool ok = k < n_tok && (w ? slive1 : slive0);
-                            rv[i][w] = ok ? raw_load<TDt>(vt, k * vs + sc + w) : 0u;
-                            rx[i][w] = ok ? raw_load<TIn>(xt, k * xs + sc + w) : 0u;
-                            rg[i][w] = ok ? raw_load<TIn>(yt, k * ys + sc + w) : 0u;
-                            rz[i][w] = ok && a.z ? raw_load<TIn>(zt, k * zs + sc + w) : 0u;
+                        if constexpr (kPacked) {
+                            rv[i].load(vt, k * vs + sc);
+                            rx[i].load(xt, k * xs + sc);
+                            rg[i].load(yt, k * ys + sc);
+                            if (a.z) rz[i].load(zt, k * zs + sc);
                         }
+                    } else {
+                        const bool ok0 = slive0 && k < n_tok, ok1 = slive1 && ok0;
+                        rv[i].load(vt, k * vs + sc, ok0, ok1);
+                        rx[i].load(xt, k * xs + sc, ok0, ok1);
+                        rg[i].load(yt, k * ys + sc, ok0, ok1);
+                        rz[i].load(zt, k * zs + sc, ok0 && a.z, ok1 && a.z);
                     }
                 }
 #pragma unroll
                 for (int i = 0; i < kStep; ++i) {
                     const int k = k0 + i * RS;
-                    f32x2 v = dt_value2(a.dtp, pair_value<TDt>(rv[i]), bias2);
+                    f32x2 v = dt_value2(a.dtp, rv[i].value(), bias2);
                     if (k >= n_tok) v = pack2(0.f, 0.f);
-                    const f32x2 u = mul2(v, pair_value<TIn>(rx[i]));
-                    f32x2 g = pair_value<TIn>(rg[i]);
-                    if (a.z) g = mul2(g, silu2(pair_value<TIn>(rz[i])));
+                    const f32x2 u = mul2(v, rx[i].value());
+                    f32x2 g = rg[i].value();
+                    if (a.z) g = mul2(g, silu2(rz[i].value()));
                     if (KC % (RS * kStep) && k >= KC) break;
                     *reinterpret_cast<float4 *>(&s_vu[k * CB + sc]) = make_float4(lo2(v), lo2(u), hi2(v), hi2(u));
                     *reinterpret_cast<float2 *>(&s_g[k * CB + sc]) = make_float2(lo2(g), hi2(g));
@@ -336,32 +336,34 @@ selective_scan_bwd_kernel(SelScanBwdArgs b, int ctas)
 #pragma unroll 1
             for (int sub = last; sub >= 0; --sub) {
                 // inputs of the tokens that this lane finishes
-                uint32_t rv[kLeft][2], rx[kLeft][2], rg[kLeft][2], rz[kLeft][2];
+                RawPair<TDt, kPacked> rv[kLeft];
+                RawPair<TIn, kPacked> rx[kLeft], rg[kLeft], rz[kLeft];
                 bool mine[kLeft];
 #pragma unroll
                 for (int i = 0; i < kLeft; ++i) {
                     const int t = sub * kSub + first + i;
                     mine[i] = t < n_tok && dc < cend && j % kSame == 0;
-#pragma unroll
-                    for (int w = 0; w < 2; ++w) rv[i][w] = rx[i][w] = rg[i][w] = rz[i][w] = 0u;
+                    rv[i].zero();
+                    rx[i].zero();
+                    rg[i].zero();
+                    rz[i].zero();
                     if (!mine[i]) continue;
                     if (pair_in) {
-                        pair_load(vt, t * vs + ch0, rv[i]);
-                        pair_load(xt, t * xs + ch0, rx[i]);
-                        if (a.z) {
-                            pair_load(yt, t * ys + ch0, rg[i]);
-                            pair_load(zt, t * zs + ch0, rz[i]);
+                        if constexpr (kPacked) {
+                            rv[i].load(vt, t * vs + ch0);
+                            rx[i].load(xt, t * xs + ch0);
+                            if (a.z) {
+                                rg[i].load(yt, t * ys + ch0);
+                                rz[i].load(zt, t * zs + ch0);
+                            }
                         }
                     } else {
-#pragma unroll
-                        for (int w = 0; w < CS; ++w) {
-                            if (dc + w >= cend) break;
-                            rv[i][w] = raw_load<TDt>(vt, t * vs + ch0 + w);
-                            rx[i][w] = raw_load<TIn>(xt, t * xs + ch0 + w);
-                            if (a.z) {
-                                rg[i][w] = raw_load<TIn>(yt, t * ys + ch0 + w);
-                                rz[i][w] = raw_load<TIn>(zt, t * zs + ch0 + w);
-                            }
+                        const bool two = CS == 2 && dc + 1 < cend;
+                        rv[i].load(vt, t * vs + ch0, true, two);
+                        rx[i].load(xt, t * xs + ch0, true, two);
+                        if (a.z) {
+                            rg[i].load(yt, t * ys + ch0, true, two);
+                            rz[i].load(zt, t * zs + ch0, true, two);
                         }
                     }
                 }
@@ -423,19 +425,19 @@ selective_scan_bwd_kernel(SelScanBwdArgs b, int ctas)
                     float tv[CS], tu[CS], tg[CS];
                     load_vu(t, tv, tu);
                     load_g(t, tg);
-                    const f32x2 x = pair_value<TIn>(rx[i]), vv = pack2(tv[0], tv[q1]), gg = pack2(tg[0], tg[q1]);
+                    const f32x2 x = rx[i].value(), vv = pack2(tv[0], tv[q1]), gg = pack2(tg[0], tg[q1]);
                     const f32x2 w = pack2(ws_[0][i], ws_[q1][i]), y = pack2(ys_[0][i], ys_[q1][i]), qq = pack2(qs_[0][i], qs_[q1][i]);
                     const long o = (t0 + t) * a.dim + dc;
                     const f32x2 dx = fma2(w, vv, mul2(own_skip, gg));
-                    const f32x2 ddt = mul2(fma2(qq, pack2(kLn2, kLn2), mul2(w, x)), dt_slope2(a.dtp, pair_value<TDt>(rv[i]), own_bias));
+                    const f32x2 ddt = mul2(fma2(qq, pack2(kLn2, kLn2), mul2(w, x)), dt_slope2(a.dtp, rv[i].value(), own_bias));
                     store_pair(static_cast<TIn *>(b.dx) + o, dx, pair_out, CS == 2 && dc + 1 < cend);
                     store_pair(static_cast<TDt *>(b.ddt) + o, ddt, pair_out, CS == 2 && dc + 1 < cend);
                     if (a.z) {
-                        const f32x2 z = pair_value<TIn>(rz[i]), one = pack2(1.f, 1.f);
+                        const f32x2 z = rz[i].value(), one = pack2(1.f, 1.f);
                         const f32x2 e = add2(ex2_pair(mul2(z, pack2(-kLog2e, -kLog2e))), one);
                         const f32x2 sg = pack2(rcp_approx(lo2(e)), rcp_approx(hi2(e)));
                         const f32x2 slope = mul2(sg, fma2(z, fma2(sg, pack2(-1.f, -1.f), one), one));
-                        store_pair(static_cast<TIn *>(b.dz) + o, mul2(mul2(pair_value<TIn>(rg[i]), fma2(own_skip, x, y)), slope),
+                        store_pair(static_cast<TIn *>(b.dz) + o, mul2(mul2(rg[i].value(), fma2(own_skip, x, y)), slope),
                                    pair_out, CS == 2 && dc + 1 < cend);
                     }
                     sum_D = fma2(gg, x, sum_D);
@@ -565,23 +567,28 @@ struct BwdPlan {
     size_t bytes() const { return 2 * bytes_B + bytes_A + 2 * bytes_D + bytes_carry; }
 };
 
+template <typename TIn, typename TDt, int R, int L, int CS, bool kPacked>
+cudaError_t launch_packed(const SelScanBwdArgs &b, const BwdPlan &p, cudaStream_t stream)
+{
+    using S = BwdShape<R, L, CS>;
+    const auto main = selective_scan_bwd_kernel<TIn, TDt, R, L, CS, false, kPacked>;
+    const auto carry = selective_scan_bwd_kernel<TIn, TDt, R, L, CS, true, kPacked>;
+    const long long tiles = (long long)p.gtiles * b.f.ngroups;
+    if (tiles * p.units > 0x7fffffffLL) return cudaErrorInvalidValue;
+    if (const cudaError_t e = cudaFuncSetAttribute(main, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::kBytes)) return e;
+    if (p.span) {
+        if (const cudaError_t e = cudaFuncSetAttribute(carry, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::kStaged)) return e;
+        carry<<<(unsigned)(tiles * p.units), kBwdThreads, S::kStaged, stream>>>(b, p.units);
+    }
+    main<<<(unsigned)(tiles * p.ctas), kBwdThreads, S::kBytes, stream>>>(b, p.ctas);
+    return cudaGetLastError();
+}
+
 template <typename TIn, typename TDt, int R, int L, int CS>
 cudaError_t launch_shape(const SelScanBwdArgs &b, const BwdPlan &p, cudaStream_t stream)
 {
-    using S = BwdShape<R, L, CS>;
-    const cudaError_t e = cudaFuncSetAttribute(selective_scan_bwd_kernel<TIn, TDt, R, L, CS, false>,
-                                               cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::kBytes);
-    if (e) return e;
-    const long long tiles = (long long)p.gtiles * b.f.ngroups;
-    if (tiles * p.units > 0x7fffffffLL) return cudaErrorInvalidValue;
-    if (p.span) {
-        const cudaError_t e2 = cudaFuncSetAttribute(selective_scan_bwd_kernel<TIn, TDt, R, L, CS, true>,
-                                                    cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::kStaged);
-        if (e2) return e2;
-        selective_scan_bwd_kernel<TIn, TDt, R, L, CS, true><<<(unsigned)(tiles * p.units), kBwdThreads, S::kStaged, stream>>>(b, p.units);
-    }
-    selective_scan_bwd_kernel<TIn, TDt, R, L, CS, false><<<(unsigned)(tiles * p.ctas), kBwdThreads, S::kBytes, stream>>>(b, p.ctas);
-    return cudaGetLastError();
+    return b.f.pairs ? launch_packed<TIn, TDt, R, L, CS, true>(b, p, stream)
+                     : launch_packed<TIn, TDt, R, L, CS, false>(b, p, stream);
 }
 
 // Lanes per channel for d_state (R = 4 states a lane, 8 above 128).
@@ -627,15 +634,15 @@ BwdPlan make_plan(int nseq, long T, int dim, int d_state, int ngroups)
         }
     }
     p.ctas = p.span || p.units < kMaxCtas ? p.units : kMaxCtas;
-    // One or two sets of channels a warp: two share the loads of B and C and the sums over the channels (a
-    // quarter less time an element when the device is full), one makes twice as many CTAs.  4 x 2048 tokens of
-    // 8192 channels with 16 states: 512 CTAs of two sets leave 68 for a second round, 2.41 ms, against 2.27 ms
-    // for 1024 of one; 16 x 512 tokens: 1.79 against 2.16 ms.
+    // One or two sets of channels a warp: two share the loads of B and C and the sums over the channels, one
+    // makes twice as many CTAs.  Measured: 4 x 2048 tokens of 8192 channels with 16 states, 2.32 ms with one set
+    // (1024 CTAs, 1.7 rounds), 2.11 with two (512, 1.15 rounds); 16 x 512 tokens, 1.60 ms with two (2.16 with
+    // one); 5 x 140 tokens of 1002 channels, 0.076 ms with one (160 CTAs), 0.100 with two (80).
     p.cs = 1;
     if (L > 1 && d_state <= 128) {
-        static const double share1[] = {0., 0.5, 0.68, 0.84, 1.}, share2[] = {0., 0.6, 0.75, 1.};
+        static const double share1[] = {0., 0.45, 0.55, 0.8, 1.}, share2[] = {0., 0.6, 0.75, 1.};
         const double one = rounds((long long)tiles_of(1) * ngroups * p.ctas, sms, 4, share1);
-        const double two = 1.22 * rounds((long long)tiles_of(2) * ngroups * p.ctas, sms, 3, share2);
+        const double two = 1.06 * rounds((long long)tiles_of(2) * ngroups * p.ctas, sms, 3, share2);
         if (two < one) p.cs = 2;
     }
     p.gtiles = tiles_of(p.cs);
