@@ -361,6 +361,4 @@ __device__ __forceinline__ int longest_first(const SelScanArgs &a, int u, int *s
     __syncthreads();
     return *shared;
 }
-constexpr int kMaxRanked = 64;
-
 }  // namespace ssm

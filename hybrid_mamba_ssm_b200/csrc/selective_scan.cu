@@ -456,13 +456,27 @@ cudaError_t launch_types(const SelScanArgs &a, cudaStream_t stream)
 // Lanes of a warp that share a channel.
 static int lanes_for(int N) { return N <= 4 ? 1 : N <= 8 ? 2 : N <= 16 ? 4 : N <= 32 ? 8 : N <= 64 ? 16 : 32; }
 
+// Tokens of a segment (0: sequences stay whole), for kernels whose CTAs of whole
+// sequences would fill `fill` of the device: below a half, as many segments as
+// fill it, of at least kSavedEvery tokens, if that is half as many again as
+// there are sequences.
+int segment_span(int nseq, long T, double fill)
+{
+    if (nseq < 1 || fill >= 0.5) return 0;
+    long segments = (long)(nseq / fill);
+    if (segments > T / kSavedEvery) segments = T / kSavedEvery;
+    if (segments > 256) segments = 256;
+    if (segments < 2 || segments <= nseq + nseq / 2) return 0;
+    const long n = (T + segments - 1) / segments;
+    return (int)((n + kSavedEvery - 1) / kSavedEvery * kSavedEvery);
+}
+
 // A sequence is a chain of its tokens: nseq * dim channels give
 // nseq * dim * lanes / 32 warps, however long it is.  Cutting sequences costs
-// the first pass over the segments (about 0.6 of the work again), so it is
-// done where the chains fill less than a third of the warps that the device
-// holds, into segments of at least 128 tokens, as many as fill it.  (1 x 32768
-// tokens, 2048 channels of 16 states: 2.8 ms as one chain, 0.9 ms cut.)
-// Returns the number of units, 0 for whole sequences.
+// the first pass over the segments, about 0.6 of their work again (1 x 32768
+// tokens, 2048 channels of 16 states: 2.8 ms as one chain, 0.9 ms cut; 600
+// tokens in 4 sequences of 700 channels: 82 and 31 us).  Returns the number of
+// units, 0 for whole sequences.
 int selective_scan_segments(int nseq, long T, int dim, int d_state, int ngroups, int *span)
 {
     *span = 0;
@@ -472,15 +486,9 @@ int selective_scan_segments(int nseq, long T, int dim, int d_state, int ngroups,
         cudaGetLastError();
         return 0;
     }
-    const double warps = (double)dim * lanes_for(d_state) / 32, room = 28.0 * sms;
-    if (warps * nseq * 3 > room) return 0;
-    long segments = (long)(room / warps);
-    if (segments > T / 128) segments = T / 128;
-    if (segments > 256) segments = 256;
-    if (segments < 3 || segments <= 2L * nseq) return 0;
-    const long n = (T + segments - 1) / segments;
-    *span = (int)((n + kSavedEvery - 1) / kSavedEvery * kSavedEvery);
-    return (int)(T / *span + nseq);
+    const double warps = (double)dim * lanes_for(d_state) / 32;
+    *span = segment_span(nseq, T, warps * nseq / (28. * sms));
+    return *span ? (int)(T / *span + nseq) : 0;
 }
 
 cudaError_t launch_selective_scan(const SelScanArgs &a, cudaStream_t stream)

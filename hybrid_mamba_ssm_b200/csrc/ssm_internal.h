@@ -171,6 +171,8 @@ struct SelScanArgs {
 // Sequence s starts at row lo / kSavedEvery + s: floor(hi / K) - floor(lo / K)
 // + 1 >= ceil((hi - lo) / K), so sequences never share a row.
 constexpr int kSavedEvery = 32;
+// Packed batches of at most this many sequences are looked at by length.
+constexpr int kMaxRanked = 64;
 inline long saved_rows(long T, int nseq) { return T / kSavedEvery + nseq; }
 
 struct SelScanBwdArgs {
@@ -185,6 +187,7 @@ struct SelScanBwdArgs {
     float *part_A;                // [CTAs per tile][dim][d_state]
     float *part_D, *part_bias;    // [CTAs per tile][dim]
 };
+int segment_span(int nseq, long T, double fill);
 int selective_scan_segments(int nseq, long T, int dim, int d_state, int ngroups, int *span);
 cudaError_t launch_selective_scan(const SelScanArgs &a, cudaStream_t stream);
 size_t selective_scan_bwd_workspace(int nseq, long T, int dim, int d_state, int ngroups);
