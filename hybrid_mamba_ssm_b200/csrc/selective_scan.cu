@@ -11,12 +11,24 @@
 // one exponential and four fp32 multiply-adds.
 //
 // Layout of the work: L lanes of a warp share a channel, each keeping R of its
-// states in registers as packed pairs; a CTA of 128 threads takes 128 / L
-// channels of one group.  Tokens go through shared memory in tiles: each
-// (token, channel) is loaded, its step size transformed and multiplied by x
-// exactly once, then read by the channel's L lanes, while the next tile's
-// global loads are in flight.  The sums over n of a few tokens are exchanged
-// together (reduce_lanes), so they cost about one shuffle per token and lane.
+// states in registers as packed pairs, of Q channels; a CTA of 128 threads takes
+// Q 128 / L channels of one group.  Tokens go through shared memory in tiles:
+// each (token, channel) is loaded, its step size transformed and multiplied by x
+// exactly once, then read by the channel's L lanes, while the next tile's global
+// loads are in flight.  Up to four partial sums over n a (token, channel) are
+// left to the step that writes y.
+//
+// What bounds it (ncu, 4096 tokens of 8192 channels, 16 states, bf16): the
+// shared-memory pipe at 76 % of its cycles, of which B and C, read by every
+// lane for its own states, are two thirds; the special-function unit at 50 %
+// (one exponential an element and three a (token, channel): 0.30 ms for 4 x
+// 2048 tokens if it were the bound); issue slots at 57 %; HBM at 10 %.  4 x 2048
+// tokens take 0.53 ms, 1 x 32768 of 2048 channels 0.90 ms.
+// Q = 2 halves the reads of B and C but also the warps: 0.62 ms against 0.53 at
+// 16 states, where seven CTAs an SM hide the latencies, but 0.48 against 0.63 ms
+// at 32 states (4 x 2048 x 4096), 0.40 against 0.49 at 64 (4 x 1024 x 4096) and
+// 0.92 against 1.92 at 256 (4 x 1024 x 2048), where few channels share a tile of
+// B and C.  Q = 4 is slower at all of them.
 #include <type_traits>
 
 #include "selective.cuh"
@@ -445,10 +457,10 @@ cudaError_t launch_types(const SelScanArgs &a, cudaStream_t stream)
     if (N <= 4) return launch_shape<TIn, TDt, 4, 1, 1>(a, stream);
     if (N <= 8) return launch_shape<TIn, TDt, 4, 2, 1>(a, stream);
     if (N <= 16) return launch_shape<TIn, TDt, 4, 4, 1>(a, stream);
-    if (N <= 32) return launch_shape<TIn, TDt, 4, 8, 1>(a, stream);
-    if (N <= 64) return launch_shape<TIn, TDt, 4, 16, 1>(a, stream);
-    if (N <= 128) return launch_shape<TIn, TDt, 4, 32, 1>(a, stream);
-    return launch_shape<TIn, TDt, 8, 32, 1>(a, stream);
+    if (N <= 32) return launch_shape<TIn, TDt, 4, 8, 2>(a, stream);
+    if (N <= 64) return launch_shape<TIn, TDt, 4, 16, 2>(a, stream);
+    if (N <= 128) return launch_shape<TIn, TDt, 4, 32, 2>(a, stream);
+    return launch_shape<TIn, TDt, 8, 32, 2>(a, stream);
 }
 
 }  // namespace
