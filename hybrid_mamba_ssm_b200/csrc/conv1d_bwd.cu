@@ -40,13 +40,9 @@ inline int walk_tokens(long T, int dim) { return T * dim < 2L * 148 * 128 * (2 *
 
 // Raw values of channels c, c + 1 of a row (the second only where it exists).
 template <typename T, bool kPair>
-__device__ __forceinline__ void load_two(const T *row, int c, bool both, uint32_t (&r)[2]) {
-    if constexpr (kPair) {
-        pair_load(row, c, r);
-    } else {
-        r[0] = raw_load<T>(row, c);
-        r[1] = both ? raw_load<T>(row, c + 1) : 0u;
-    }
+__device__ __forceinline__ void load_two(const T *row, int c, bool both, RawPair<T, kPair> &r) {
+    if constexpr (kPair) r.load(row, c);
+    else r.load(row, c, true, both);
 }
 template <typename T, bool kPair>
 __device__ __forceinline__ void store_two(T *row, int c, bool both, f32x2 v) {
@@ -62,7 +58,7 @@ __device__ __forceinline__ void store_two(T *row, int c, bool both, f32x2 v) {
 
 // kPair: dim is even, so two channels are one aligned access.
 template <typename T, int K, bool kPair>
-__global__ void __launch_bounds__(kBwdThreads, K <= 4 ? 4 : 3)
+__global__ void __launch_bounds__(kBwdThreads, K <= 4 ? 5 : 3)
 conv1d_bwd_kernel(ConvBwdArgs a, int ctiles, int walk)
 {
     constexpr int H = K - 1;                  // history entries
@@ -134,12 +130,13 @@ conv1d_bwd_kernel(ConvBwdArgs a, int ctiles, int walk)
         for (int k = 0; k < H; ++k) {
             dp[k] = pack2(0.f, 0.f);
             const long i = t - H + k;
-            uint32_t r[2] = {0u, 0u};
+            RawPair<T, kPair> r;
+            r.zero();
             if (i >= lo) load_two<T, kPair>(x + i * a.dim, c, both, r);
-            win[k] = pair_value<T>(r);
+            win[k] = r.value();
             if (i < lo && init && i >= lo - H) win[k] = history(init, s, i - lo + H);
         }
-        uint32_t rx[kGroup][2], rg[kGroup][2];
+        RawPair<T, kPair> rx[kGroup], rg[kGroup];
         auto fetch = [&](int i0) {                              // 32-bit offsets from the walk's first row
             if (i0 + kGroup <= npast) {
 #pragma unroll
@@ -150,7 +147,8 @@ conv1d_bwd_kernel(ConvBwdArgs a, int ctiles, int walk)
             } else {
 #pragma unroll
                 for (int i = 0; i < kGroup; ++i) {
-                    rx[i][0] = rx[i][1] = rg[i][0] = rg[i][1] = 0u;
+                    rx[i].zero();
+                    rg[i].zero();
                     if (i0 + i < npast) {
                         load_two<T, kPair>(xt, (i0 + i) * a.dim + c, both, rx[i]);
                         load_two<T, kPair>(gt, (i0 + i) * a.dim + c, both, rg[i]);
@@ -187,8 +185,8 @@ conv1d_bwd_kernel(ConvBwdArgs a, int ctiles, int walk)
             f32x2 g[kGroup];
 #pragma unroll
             for (int i = 0; i < kGroup; ++i) {
-                win[H + i] = pair_value<T>(rx[i]);
-                g[i] = pair_value<T>(rg[i]);
+                win[H + i] = rx[i].value();
+                g[i] = rg[i].value();
             }
             if (i0 + kGroup < npast) fetch(i0 + kGroup);
             group_dpre(g);

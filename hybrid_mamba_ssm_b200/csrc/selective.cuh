@@ -243,20 +243,6 @@ struct RawPair {
     }
 };
 
-// Two adjacent values.  pair_load wants an address aligned to both; either way
-// the registers hold what pair_value takes: a bf16 pair is one register, or
-// two with a value in the low half of each.
-template <typename T>
-__device__ __forceinline__ void pair_load(const T *p, int i, uint32_t (&r)[2]) {
-    if constexpr (sizeof(T) == 2) {
-        r[0] = *reinterpret_cast<const uint32_t *>(p + i);
-        r[1] = 0u;
-    } else {
-        const uint2 q = *reinterpret_cast<const uint2 *>(p + i);
-        r[0] = q.x;
-        r[1] = q.y;
-    }
-}
 // Stores v[0], and v[1] when `both`: as one aligned access when `aligned`.
 template <typename T>
 __device__ __forceinline__ void store_pair(T *p, f32x2 v, bool aligned, bool both) {
@@ -267,13 +253,6 @@ __device__ __forceinline__ void store_pair(T *p, f32x2 v, bool aligned, bool bot
         store_out(p, lo2(v));
         if (both) store_out(p + 1, hi2(v));
     }
-}
-template <typename T>
-__device__ __forceinline__ f32x2 pair_value(const uint32_t (&r)[2]) {
-    if constexpr (sizeof(T) == 2)
-        return pack2(__uint_as_float(r[0] << 16), __uint_as_float((r[0] & 0xffff0000u) | (r[1] << 16)));
-    else
-        return pack2(__uint_as_float(r[0]), __uint_as_float(r[1]));
 }
 template <typename T>
 __device__ __forceinline__ float ld_as(const void *p, long i) {
