@@ -58,7 +58,7 @@ __device__ __forceinline__ void store_two(T *row, int c, bool both, f32x2 v) {
 
 // kPair: dim is even, so two channels are one aligned access.
 template <typename T, int K, bool kPair>
-__global__ void __launch_bounds__(kBwdThreads, K <= 4 ? 5 : 3)
+__global__ void __launch_bounds__(kBwdThreads, K <= 4 ? 4 : 2)
 conv1d_bwd_kernel(ConvBwdArgs a, int ctiles, int walk)
 {
     constexpr int H = K - 1;                  // history entries
