@@ -11,7 +11,10 @@
 // its B and C once for all of them.  The L lanes of a channel share the scalar
 // work: a lane transforms the step size of its own set(s) of channels and hands
 // v and v x to the others by shuffles, and the sums over n end in that same lane
-// (reduce_lanes), which writes that y.
+// (reduce_lanes), which writes that y.  256 rows of 8192 channels, 16 states:
+// 59 us, 4.8 TB/s (the loads' latency: 40 % occupancy by registers).  Four rows
+// of 64 channels a CTA, which share a read of A, took 72 us: 4 KB runs from four
+// places, and four sets of B and C.
 #include "selective.cuh"
 
 namespace ssm {
