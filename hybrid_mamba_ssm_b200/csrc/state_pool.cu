@@ -2,8 +2,8 @@
 // compacted, in any number of pools (one per layer and kind of state) by one
 // launch.
 //
-// Every thread owns one column of a pool: the same 16 bytes (or 4, or 1, by
-// the pools' alignment) of every row.  It applies the list of row copies to
+// Every thread owns one column of a pool: the same 16 bytes (or 8 .. 1, by
+// that pool's alignment) of every row.  It applies the list of row copies to
 // its column in order, so the list has the meaning of a loop over it whatever
 // rows it repeats or chains, without an ordering between threads.  kBatch
 // copies are loaded before any is stored, unless one of them reads a row that
@@ -25,6 +25,7 @@ struct PoolList {
     char *base[kPoolsPerLaunch];
     long stride[kPoolsPerLaunch];
     long cols[kPoolsPerLaunch];                  // columns of a row
+    uint8_t width[kPoolsPerLaunch];              // bytes of a column
     unsigned first_block[kPoolsPerLaunch + 1];   // blocks of pool p: [first_block[p], first_block[p + 1])
 };
 
@@ -42,17 +43,24 @@ __device__ __forceinline__ U *cell(char *base, long stride, int row) {
     return reinterpret_cast<U *>(base + (long)row * stride);
 }
 
-template <typename U>
-__global__ void __launch_bounds__(kPoolThreads)
-pool_copy_kernel(const __grid_constant__ PoolList l, int npools, int max_slots, int n, const int32_t *src,
-                 const int32_t *dst, const int32_t *count, int *status)
-{
-    const int p = pool_of(l, npools, blockIdx.x);
+// Calls f(a value of the column's type, the column's address in row 0, the row stride).
+template <typename F>
+__device__ __forceinline__ void for_column(const PoolList &l, int npools, F f) {
+    const int p = pool_of(l, npools, blockIdx.x), width = l.width[p];
     const long col = (long)(blockIdx.x - l.first_block[p]) * kPoolThreads + threadIdx.x;
-    if (count) n = min(n, *count);
     if (col >= l.cols[p]) return;
-    char *base = l.base[p] + col * (long)sizeof(U);
-    const long stride = l.stride[p];
+    char *base = l.base[p] + col * width;
+    if (width == 16) f(uint4{}, base, l.stride[p]);
+    else if (width == 8) f(uint2{}, base, l.stride[p]);
+    else if (width == 4) f(uint32_t{}, base, l.stride[p]);
+    else if (width == 2) f(uint16_t{}, base, l.stride[p]);
+    else f(uint8_t{}, base, l.stride[p]);
+}
+
+template <typename U>
+__device__ __forceinline__ void copy_rows(char *base, long stride, int max_slots, int n, const int32_t *src,
+                                          const int32_t *dst, int *status)
+{
     for (int i0 = 0; i0 < n; i0 += kBatch) {
         int s[kBatch], d[kBatch];
 #pragma unroll
@@ -88,22 +96,28 @@ pool_copy_kernel(const __grid_constant__ PoolList l, int npools, int max_slots, 
     }
 }
 
-template <typename U>
+__global__ void __launch_bounds__(kPoolThreads)
+pool_copy_kernel(const __grid_constant__ PoolList l, int npools, int max_slots, int n, const int32_t *src,
+                 const int32_t *dst, const int32_t *count, int *status)
+{
+    if (count) n = min(n, *count);
+    for_column(l, npools, [&](auto u, char *base, long stride) {
+        copy_rows<decltype(u)>(base, stride, max_slots, n, src, dst, status);
+    });
+}
+
 __global__ void __launch_bounds__(kPoolThreads)
 pool_zero_kernel(const __grid_constant__ PoolList l, int npools, int max_slots, int n, const int32_t *rows,
                  int *status)
 {
-    const int p = pool_of(l, npools, blockIdx.x);
-    const long col = (long)(blockIdx.x - l.first_block[p]) * kPoolThreads + threadIdx.x;
-    if (col >= l.cols[p]) return;
-    char *base = l.base[p] + col * (long)sizeof(U);
-    const U zero{};
-    for (int i = 0; i < n; ++i) {
-        const int r = __ldg(rows + i);
-        if (r < 0) continue;
-        if (r >= max_slots) report_status(status, kStatusDeviceInput);
-        else *cell<U>(base, l.stride[p], r) = zero;
-    }
+    for_column(l, npools, [&](auto u, char *base, long stride) {
+        for (int i = 0; i < n; ++i) {
+            const int r = __ldg(rows + i);
+            if (r < 0) continue;
+            if (r >= max_slots) report_status(status, kStatusDeviceInput);
+            else *cell<decltype(u)>(base, stride, r) = u;
+        }
+    });
 }
 
 // Plan of a compaction, one CTA.  The distinct live rows are counted (n); the
@@ -169,18 +183,16 @@ pool_plan_kernel(int32_t *table, int nrows, int max_slots, int32_t *map, int32_t
     }
 }
 
-// Widest column that every pool's rows split into (16, 4 or 1 bytes).
-int column_bytes(const PoolArgs &a)
+// Widest column that the pool's rows split into.
+int column_bytes(const PoolRows &r)
 {
-    uintptr_t bits = 0;
-    for (int p = 0; p < a.npools; ++p)
-        bits |= reinterpret_cast<uintptr_t>(a.pools[p].base) | (uintptr_t)a.pools[p].row_bytes | (uintptr_t)a.pools[p].stride;
-    return bits % 16 == 0 ? 16 : bits % 4 == 0 ? 4 : 1;
+    const uintptr_t bits = reinterpret_cast<uintptr_t>(r.base) | (uintptr_t)r.row_bytes | (uintptr_t)r.stride;
+    return bits % 16 == 0 ? 16 : bits % 8 == 0 ? 8 : bits % 4 == 0 ? 4 : bits % 2 == 0 ? 2 : 1;
 }
 
 // Calls f(list, pools of the list, blocks) for lists of at most kPoolsPerLaunch pools.
 template <typename F>
-cudaError_t for_lists(const PoolArgs &a, int width, F f)
+cudaError_t for_lists(const PoolArgs &a, F f)
 {
     for (int p0 = 0; p0 < a.npools; p0 += kPoolsPerLaunch) {
         PoolList l;
@@ -190,7 +202,8 @@ cudaError_t for_lists(const PoolArgs &a, int width, F f)
             const PoolRows &r = a.pools[p0 + p];
             l.base[p] = r.base;
             l.stride[p] = r.stride;
-            l.cols[p] = r.row_bytes / width;
+            l.width[p] = (uint8_t)column_bytes(r);
+            l.cols[p] = r.row_bytes / l.width[p];
             l.first_block[p] = (unsigned)blocks;
             blocks += (unsigned long long)((l.cols[p] + kPoolThreads - 1) / kPoolThreads);
             if (blocks > 0x7fffffffULL) return cudaErrorInvalidValue;
@@ -206,21 +219,15 @@ cudaError_t for_lists(const PoolArgs &a, int width, F f)
 
 cudaError_t launch_pool_copy(const PoolArgs &a, cudaStream_t stream)
 {
-    const int w = column_bytes(a);
-    return for_lists(a, w, [&](const PoolList &l, int m, unsigned blocks) {
-        if (w == 16) pool_copy_kernel<uint4><<<blocks, kPoolThreads, 0, stream>>>(l, m, a.max_slots, a.n, a.src, a.dst, a.count, a.status_dev);
-        else if (w == 4) pool_copy_kernel<uint32_t><<<blocks, kPoolThreads, 0, stream>>>(l, m, a.max_slots, a.n, a.src, a.dst, a.count, a.status_dev);
-        else pool_copy_kernel<uint8_t><<<blocks, kPoolThreads, 0, stream>>>(l, m, a.max_slots, a.n, a.src, a.dst, a.count, a.status_dev);
+    return for_lists(a, [&](const PoolList &l, int m, unsigned blocks) {
+        pool_copy_kernel<<<blocks, kPoolThreads, 0, stream>>>(l, m, a.max_slots, a.n, a.src, a.dst, a.count, a.status_dev);
     });
 }
 
 cudaError_t launch_pool_zero(const PoolArgs &a, cudaStream_t stream)
 {
-    const int w = column_bytes(a);
-    return for_lists(a, w, [&](const PoolList &l, int m, unsigned blocks) {
-        if (w == 16) pool_zero_kernel<uint4><<<blocks, kPoolThreads, 0, stream>>>(l, m, a.max_slots, a.n, a.dst, a.status_dev);
-        else if (w == 4) pool_zero_kernel<uint32_t><<<blocks, kPoolThreads, 0, stream>>>(l, m, a.max_slots, a.n, a.dst, a.status_dev);
-        else pool_zero_kernel<uint8_t><<<blocks, kPoolThreads, 0, stream>>>(l, m, a.max_slots, a.n, a.dst, a.status_dev);
+    return for_lists(a, [&](const PoolList &l, int m, unsigned blocks) {
+        pool_zero_kernel<<<blocks, kPoolThreads, 0, stream>>>(l, m, a.max_slots, a.n, a.dst, a.status_dev);
     });
 }
 

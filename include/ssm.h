@@ -615,7 +615,8 @@ SSM_API int selective_state_update(int batch, int dim, int d_state, int ngroups,
  *                   a fixed order
  *   dinitial_state  gradient of the history entries, or NULL
  *   workspace       causal_conv1d_bwd_workspace_size(...) bytes, required
- * A sequence whose offsets are inconsistent is skipped (SSM_ERR_DEVICE_INPUT).
+ * Tokens behind an inconsistent offset are skipped (to the end of their tile;
+ * SSM_ERR_DEVICE_INPUT).
  */
 SSM_API int causal_conv1d_bwd(int nseq, int seqlen, const int32_t *cu_seqlens, int dim, int width,
                               int in_dtype, const void *dy, const void *x, const float *weight,

@@ -414,10 +414,11 @@ def make_pools(slots, kinds):
     return out
 
 
-KINDS = [[((64, 16), F), ((64, 3), BF)], [((33,), torch.int8), ((7, 3), BF)], [((5,), F)] * 70, [((1,), torch.uint8)]]
+KINDS = [[((64, 16), F), ((64, 3), BF)], [((33,), torch.int8), ((7, 3), BF)], [((5,), F)] * 70, [((1,), torch.uint8)],
+         [((16, 4), F), ((2, 3), F), ((9,), F), ((3,), BF), ((11,), torch.uint8)]]
 
 
-@pytest.mark.parametrize("kinds", KINDS, ids=["states", "odd", "many", "bytes"])
+@pytest.mark.parametrize("kinds", KINDS, ids=["states", "odd", "many", "bytes", "every-width"])
 @pytest.mark.parametrize("pairs", [[(0, 3), (0, 4), (1, 5)], [(0, 1), (1, 2), (2, 0), (0, 1)], [(4, 4), (-1, 2), (3, -2), (9, 0)],
                                    [(i % 4, 4 + i % 6) for i in range(40)], [(i, i + 1) for i in range(9)], []])
 def test_pool_copy_is_the_loop(kinds, pairs):
