@@ -402,7 +402,8 @@ selective_scan_kernel(SelScanArgs a)
     }
     if (kMode == kRangeOut && w.k > 0) {
         load_all(a.range_state, w.base, h);
-        for (int i = 1; i < w.k; ++i) {
+#pragma unroll 4
+        for (int i = 1; i < w.k; ++i) {                    // (loads of four segments in flight)
             f32x2 e[Q][P];
             load_all(a.range_state, w.base + i, e);
 #pragma unroll
@@ -469,18 +470,27 @@ cudaError_t launch_types(const SelScanArgs &a, cudaStream_t stream)
 static int lanes_for(int N) { return N <= 4 ? 1 : N <= 8 ? 2 : N <= 16 ? 4 : N <= 32 ? 8 : N <= 64 ? 16 : 32; }
 
 // Tokens of a segment (0: sequences stay whole), for kernels whose CTAs of whole
-// sequences would fill `fill` of the device: below a half, as many segments as
+// sequences would fill `fill` of the device.  Below a half: as many segments as
 // fill it, of at least kSavedEvery tokens, if that is half as many again as
-// there are sequences.
+// there are sequences.  Up to three times the device: segments a quarter longer
+// than the mean sequence, so that of a ragged batch only the long sequences are
+// cut, whose chains would be the time of all.
 int segment_span(int nseq, long T, double fill)
 {
-    if (nseq < 1 || fill >= 0.5) return 0;
-    long segments = (long)(nseq / fill);
-    if (segments > T / kSavedEvery) segments = T / kSavedEvery;
-    if (segments > 256) segments = 256;
-    if (segments < 2 || segments <= nseq + nseq / 2) return 0;
-    const long n = (T + segments - 1) / segments;
-    return (int)((n + kSavedEvery - 1) / kSavedEvery * kSavedEvery);
+    if (nseq < 1) return 0;
+    if (fill < 0.5) {
+        long segments = (long)(nseq / fill);
+        if (segments > T / kSavedEvery) segments = T / kSavedEvery;
+        if (segments > 256) segments = 256;
+        if (segments >= 2 && segments > nseq + nseq / 2) {
+            const long n = (T / segments + kSavedEvery / 2) / kSavedEvery * kSavedEvery;
+            return (int)(n < kSavedEvery ? kSavedEvery : n);
+        }
+    }
+    const long mean = T / nseq;
+    if (fill < 3. && nseq > 1 && nseq <= kMaxRanked && mean >= 256)
+        return (int)((mean * 5 / 4 + kSavedEvery - 1) / kSavedEvery * kSavedEvery);
+    return 0;
 }
 
 // A sequence is a chain of its tokens: nseq * dim channels give

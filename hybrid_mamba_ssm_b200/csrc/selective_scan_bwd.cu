@@ -189,7 +189,8 @@ selective_scan_bwd_kernel(SelScanBwdArgs b, int ctas)
             if (w.e == hi && b.dfinal && d < cend) load_row<R>(b.dfinal + ((long)s * a.dim + d) * N, j, N, G[q]);
         }
         if (!kCarry && w.e < hi) {               // the gradient that enters from the segments behind
-            for (long m = (hi - lo - 1) / a.span; m > w.k; --m) {
+#pragma unroll 4
+            for (int m = (int)((hi - lo - 1) / a.span); m > w.k; --m) {
 #pragma unroll
                 for (int q = 0; q < CS; ++q) {
                     const int d = dc + q;
@@ -633,10 +634,9 @@ BwdPlan make_plan(int nseq, long T, int dim, int d_state, int ngroups)
     const int L = lanes_for(d_state), gdim = dim / ngroups, sms = sm_count();
     auto tiles_of = [&](int cs) { const int cb = 32 / L * cs * kWarps; return (gdim + cb - 1) / cb; };
     // Segments, where one-set CTAs of whole sequences would fill less than half of the device: as many as fill
-    // it, of at least 32 tokens.  The pass before costs about a quarter of the work again.  Measured, training
-    // steps: 701 tokens in 5 sequences of 1002 channels 129 us whole, 87 cut; 4000 in 4 of 2048 channels 1005 and
-    // 543 us.  (Cutting only the long sequences of a ragged batch that fills the device gained 5 % on one batch
-    // and lost 3 % on another; they run longest first instead.)
+    // it, of at least 32 tokens; and the long sequences of a ragged batch that fills it (segment_span).  The pass
+    // before costs about a quarter of the cut sequences' work again.  Measured, training steps: 701 tokens in 5
+    // sequences of 1002 channels 129 us whole, 87 cut; 4000 in 4 of 2048 channels 1005 and 543 us.
     const double fill = (double)tiles_of(1) * ngroups * nseq / (4. * sms);
     p.units = nseq;
     p.span = segment_span(nseq, T, fill);
@@ -651,7 +651,7 @@ BwdPlan make_plan(int nseq, long T, int dim, int d_state, int ngroups)
         static const double share1[] = {0., 0.45, 0.55, 0.8, 1.}, share2[] = {0., 0.6, 0.75, 1.};
         const double one = rounds((long long)tiles_of(1) * ngroups * p.ctas, sms, 4, share1);
         const double two = 1.06 * rounds((long long)tiles_of(2) * ngroups * p.ctas, sms, 3, share2);
-        if (two < one) p.cs = 2;
+        if (two < 0.95 * one) p.cs = 2;
     }
     p.gtiles = tiles_of(p.cs);
     auto up = [](size_t v) { return (v + 15) / 16 * 16; };
@@ -696,7 +696,11 @@ cudaError_t launch_selective_scan_bwd(SelScanBwdArgs b, void *workspace, cudaStr
     SelScanArgs &a = b.f;
     const long T = a.cu_seqlens ? (long)a.seqlen : (long)a.nseq * a.seqlen;
     const int N = a.d_state;
-    const BwdPlan p = make_plan(a.nseq, T, a.dim, N, a.ngroups);
+    BwdPlan p = make_plan(a.nseq, T, a.dim, N, a.ngroups);
+    if (!a.cu_seqlens && p.span >= a.seqlen) {       // equal lengths, nothing to cut (the workspace stays as it is)
+        p.span = 0;
+        p.ctas = p.units = a.nseq;
+    }
     char *w = static_cast<char *>(workspace);
     auto take = [&](size_t bytes) {
         float *f = reinterpret_cast<float *>(w);
