@@ -145,11 +145,9 @@ int selective_scan_fwd(int nseq, int seqlen, const int32_t *cu_seqlens, int dim,
     a.slot_idx = slot_idx; a.has_initial = has_initial_state; a.max_slots = max_slots;
     a.y = y; a.saved = saved_states; a.status_dev = status_dev;
     a.pairs = dim / ngroups % 2 == 0 && paired(rows[0]) && paired(rows[1]) && paired(rows[4]);
-    const int units = cut ? ssm::selective_scan_segments(nseq, T, dim, d_state, ngroups, &a.span) : 0;
     a.units = nseq;
-    if (!cu_seqlens && a.span >= seqlen) a.span = 0;               // equal lengths, nothing to cut
-    if (a.span) {
-        a.units = units;
+    if (cut) {
+        a.units = ssm::selective_scan_segments(nseq, T, dim, d_state, ngroups, &a.span);
         const size_t n = up16((size_t)a.units * srow * sizeof(float));
         char *w = static_cast<char *>(workspace);
         a.range_state = reinterpret_cast<float *>(w);

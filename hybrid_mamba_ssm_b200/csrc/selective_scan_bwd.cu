@@ -639,7 +639,7 @@ BwdPlan make_plan(int nseq, long T, int dim, int d_state, int ngroups)
     // sequences of 1002 channels 129 us whole, 87 cut; 4000 in 4 of 2048 channels 1005 and 543 us.
     const double fill = (double)tiles_of(1) * ngroups * nseq / (4. * sms);
     p.units = nseq;
-    p.span = segment_span(nseq, T, fill);
+    p.span = segment_span(nseq, T, fill, true);
     if (p.span) p.units = (int)(T / p.span + nseq);
     p.ctas = p.span || p.units < kMaxCtas ? p.units : kMaxCtas;
     // One or two sets of channels a warp: two share the loads of B and C and the sums over the channels, one

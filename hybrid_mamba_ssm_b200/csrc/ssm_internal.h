@@ -187,7 +187,7 @@ struct SelScanBwdArgs {
     float *part_A;                // [CTAs per tile][dim][d_state]
     float *part_D, *part_bias;    // [CTAs per tile][dim]
 };
-int segment_span(int nseq, long T, double fill);
+int segment_span(int nseq, long T, double fill, bool ragged);
 int selective_scan_segments(int nseq, long T, int dim, int d_state, int ngroups, int *span);
 cudaError_t launch_selective_scan(const SelScanArgs &a, cudaStream_t stream);
 size_t selective_scan_bwd_workspace(int nseq, long T, int dim, int d_state, int ngroups);
