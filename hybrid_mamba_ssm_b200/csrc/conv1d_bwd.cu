@@ -22,8 +22,8 @@
 // twice, from L2).  Weight and bias sums stay in registers over
 // the tile and are added up over the tiles by a second launch, in a fixed
 // order.  Bound by HBM: x and dy read once, dx written once.  16384 tokens of
-// 10240 bf16 channels, width 4: 0.24 ms (4.2 TB/s of the bytes above; 0.22 ms is
-// this kernel, at 4.7 TB/s with the parts it writes, issue slots at 53 %).  One
+// 10240 bf16 channels, width 4: 0.23 ms (4.3 TB/s of the bytes above, two launches;
+// issue slots at 53 %).  One
 // token at a time, without groups: 0.61 ms.
 #include "selective.cuh"
 
@@ -35,11 +35,16 @@ constexpr int kBwdThreads = 128;
 constexpr int kGroup = 8;
 
 // Tokens of a tile: a walk inside one sequence is `walk` tokens, K - 1 of them
-// behind the tile.  128, or 32 where that leaves fewer than two CTAs an SM (a
-// walk is a chain of its groups: 701 tokens of 1002 channels take 22 us in 24
-// CTAs of 128, 8 us in 88 of 32).
+// behind the tile.  256 where that leaves eight CTAs an SM (16384 tokens of
+// 10240 channels 233 us, 239 with 128: fewer parts to add), 128 down to two, else
+// 32 (a walk is a chain of its groups: 701 tokens of 1002 channels take 22 us in
+// 24 CTAs of 128, 8 us in 88 of 32).
 __host__ __device__ __forceinline__ int tile_tokens(int walk, int K) { return walk - (K - 1); }
-inline int walk_tokens(long T, int dim) { return T * dim < 2L * 148 * 128 * (2 * kBwdThreads) ? 32 : 128; }
+inline int walk_tokens(long T, int dim)
+{
+    const long strip = 148L * 2 * kBwdThreads;       // channels of one CTA an SM
+    return T * dim >= 8 * strip * 256 ? 256 : T * dim >= 2 * strip * 128 ? 128 : 32;
+}
 
 // Raw values of channels c, c + 1 of a row (the second only where it exists).
 template <typename T, bool kPair>

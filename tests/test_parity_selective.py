@@ -310,6 +310,40 @@ def test_scan_gradient_cut_into_segments(lens, dim, N, G):
         close(t, want[k], mag[k], n + (sum(lens) + dim if k in ("dA", "dB", "dC", "dD", "dbias") else 0), k)
 
 
+def _parts_bytes(channels, lens, dim, N, G):
+    """Workspace of whole sequences whose CTAs take `channels` channels (the parts of dB, dC, then dA, dD, the bias)."""
+    up = lambda v: (v + 15) // 16 * 16  # noqa: E731
+    tiles, n = -(-(dim // G) // channels), len(lens)
+    return 2 * up(tiles * sum(lens) * G * N * 4) + up(n * dim * N * 4) + 2 * up(n * dim * 4)
+
+
+BIG = [([int(v) for v in np.random.default_rng(8).integers(0, 9, 40)], dim, N, G)
+       for dim, N, G in [(1024, 8, 1), (1030, 16, 2), (1024, 16, 2), (520, 32, 1), (264, 64, 4), (130, 128, 2)]]
+
+
+@pytest.mark.parametrize("dtype,dt", [("bf16", "bf16"), ("f32", "f32")])
+@pytest.mark.parametrize("shape", BIG + [([200], 8192, 16, 1), ([640, 100, 40], 1024, 64, 1)], ids=ids)
+def test_scan_gradient_when_the_device_is_full(shape, dtype, dt):
+    """Two sets of channels a warp, whole sequences and cut ones: the sums over channels and sequences of many CTAs."""
+    from hybrid_mamba_ssm_b200 import ssm
+    lens, dim, N, G = shape
+    if len(lens) == 40:
+        lanes = {8: 2, 16: 4, 32: 8, 64: 16, 128: 32}[N]
+        assert ssm.selective_scan_bwd_workspace_size(40, sum(lens), dim, N, G) == _parts_bytes(256 // lanes, lens, dim, N, G)
+    p = scan_case(25, lens, dim, N, G, dtype, dt)
+    args, kw = operands(p, dtype, dt)
+    rng = np.random.default_rng(26)
+    dy, dhT = rounder(DT[dtype])(rng.standard_normal((sum(lens), dim))), rounder(F)(rng.standard_normal((len(lens), dim, N)))
+    y, _, saved = ssm.selective_scan_fwd(*args, **kw, initial_state=dev(p["h0"]), cu_seqlens=cu_of(p), save_states=True)
+    g = ssm.selective_scan_bwd(dev(dy, DT[dtype]), *args, saved, **kw, dfinal_state=dev(dhT), cu_seqlens=cu_of(p),
+                               want_dinitial=True)
+    want, mag = ref.scan_grad(p, dy, dhT), ref.scan_grad(p, dy, dhT, magnitude=True)
+    n = ref.scan_rounding(p)
+    for t, k in [(g.dx, "dx"), (g.ddt, "ddt"), (g.dA, "dA"), (g.dB, "dB"), (g.dC, "dC"), (g.dD, "dD"), (g.dz, "dz"),
+                 (g.ddt_bias, "dbias"), (g.dinitial_state, "dh0")]:
+        close(t, want[k], mag[k], n + (sum(lens) + dim if k in ("dA", "dB", "dC", "dD", "dbias") else 0), k)
+
+
 @pytest.mark.parametrize("dtype,dt", TYPES)
 @pytest.mark.parametrize("batch,dim,N,G", [(1, 64, 16, 1), (5, 130, 16, 2), (3, 33, 13, 1), (9, 7, 1, 1), (4, 12, 4, 3),
                                            (6, 20, 8, 1), (2, 24, 32, 2), (5, 10, 64, 1), (3, 6, 128, 1), (7, 5, 100, 1),
@@ -392,6 +426,27 @@ def test_conv_gradient(lens, dim, K, dtype):
         close(v, want[k], np.maximum(mag[k], flat[k]), per + many, name)
     for a, b in zip(got, again):
         assert a is None or bool((a == b).all())
+
+
+@pytest.mark.parametrize("T,dim,dtype", [(6000, 13000, "bf16"), (3000, 4097, "bf16"), (5000, 2000, "f32")])
+def test_conv_gradient_of_large_inputs(T, dim, dtype):
+    """Longer tiles: a few channels and all tokens against the reference (channels are independent)."""
+    from hybrid_mamba_ssm_b200 import ssm
+    t, K = DT[dtype], 4
+    cu = [0, T // 3, T // 3 + 1, T]
+    gen = torch.Generator(device="cuda").manual_seed(7)
+    x, dy = (torch.randn(T, dim, generator=gen, device="cuda").to(t) for _ in range(2))
+    w, b = torch.randn(dim, K, generator=gen, device="cuda") * 0.5, torch.randn(dim, generator=gen, device="cuda")
+    got = ssm.causal_conv1d_bwd(dy, x, w, b, cu_seqlens=torch.tensor(cu, dtype=torch.int32, device="cuda"))
+    pick = [0, 1, 255, 256, dim // 2, dim - 2, dim - 1]
+    p = {"x": to_np(x[:, pick]), "weight": to_np(w[pick]), "bias": to_np(b[pick]), "act": True, "init": None, "cu": cu}
+    g = to_np(dy[:, pick])
+    want, mag = ref.conv_grad(p, g, None), ref.conv_grad({**p, "act": False}, 1.1 * g, None, magnitude=True)
+    pre = sum(np.abs(p["weight"][:, k]) for k in range(K)) * np.abs(p["x"]).max() + np.abs(p["bias"])
+    per = 32 + K + (K + 2) * float(pre.max())          # as in test_conv_gradient
+    close(got[0][:, pick], want["dx"], mag["dx"], per, "dx")
+    close(got[1][pick], want["dw"], mag["dw"], per + T, "dweight")
+    close(got[2][pick], want["db"], mag["db"], per + T, "dbias")
 
 
 def test_conv_gradient_bad_offsets():
