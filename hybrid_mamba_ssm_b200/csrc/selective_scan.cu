@@ -472,13 +472,15 @@ static int lanes_for(int N) { return N <= 4 ? 1 : N <= 8 ? 2 : N <= 16 ? 4 : N <
 // Tokens of a segment (0: sequences stay whole), for kernels whose CTAs of whole
 // sequences would fill `fill` of the device.  Below a half: as many segments as
 // fill it, of at least kSavedEvery tokens, if that is half as many again as
-// there are sequences.  With `ragged`, up to three times the device: segments a
-// quarter longer than the mean sequence, so that only a ragged batch's long
-// sequences are cut, whose chains would be the time of all.  (The gradient does:
-// 4096 tokens in 6 sequences, 2048 channels of 64 states, seven draws of the
-// lengths: 1.14 to 2.24 ms whole, 1.39 to 1.69 cut.  The forward pass pays 0.6
-// of the cut work and does not: 5 sequences, 8000 tokens, 4096 channels 0.46 to
-// 0.73 ms whole, 0.54 to 0.62 cut, the same on average.)
+// there are sequences.  With `ragged`, up to three times the device: segments of
+// 5/16 of the mean sequence, so that neither a long sequence's chain nor a last
+// round of few CTAs is the time of all.  (The gradient does: 16884 tokens in 14
+// sequences of 1276 channels 1.83 ms with segments of 5/4 of the mean, 1.36 with
+// 5/8, 1.34 with 5/16, 1.30 with 5/32; 4 x 2048 tokens of 8192 channels 2.66,
+// 2.54, 2.57, 2.58 with the forward pass.  Up to six times the device it loses:
+// 8 x 2048 tokens 4.42 ms whole, 4.91 cut.  The forward pass pays 0.6 of the cut
+// work and does not: 5 sequences, 8000 tokens, 4096 channels 0.46 to 0.73 ms
+// whole, 0.54 to 0.62 cut, the same on average.)
 int segment_span(int nseq, long T, double fill, bool ragged)
 {
     if (nseq < 1) return 0;
@@ -492,8 +494,8 @@ int segment_span(int nseq, long T, double fill, bool ragged)
         }
     }
     const long mean = T / nseq;
-    if (ragged && fill < 3. && nseq > 1 && nseq <= kMaxRanked && mean >= 256)
-        return (int)((mean * 5 / 4 + kSavedEvery - 1) / kSavedEvery * kSavedEvery);
+    if (ragged && fill < 3. && nseq > 1 && nseq <= kMaxRanked && mean >= 128)
+        return (int)((mean * 5 / 16 + kSavedEvery - 1) / kSavedEvery * kSavedEvery);
     return 0;
 }
 

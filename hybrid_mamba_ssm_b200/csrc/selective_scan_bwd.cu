@@ -34,8 +34,8 @@
 // issue slots at 53 %, the shared-memory pipe at 52 %, the special-function unit
 // at 35 % (two exponentials an element and six a (token, channel)), HBM at 8 %;
 // 168 registers and 75 KB a CTA allow 12 warps an SM, whose latencies are not
-// all hidden.  16 x 512 tokens take 1.60 ms, 4 x 2048 2.11 ms (a second round of
-// CTAs), 1 x 4096 of 2048 channels with 128 states 2.50 ms.
+// all hidden.  16 x 512 tokens take 1.60 ms, 4 x 2048 2.0 ms (2.11 as whole
+// sequences, for a second round of CTAs), 1 x 4096 of 2048 channels with 128 states 2.50 ms.
 // Steps that paid: lanes finishing their own tokens instead of a second pass
 // over the chunk (2.9 -> 2.4 ms at 4 x 2048 with the next one), the sums over
 // channels by 16-byte accesses to shared memory instead of shuffles (36 -> 31
