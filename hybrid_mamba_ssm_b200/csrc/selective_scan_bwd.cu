@@ -546,6 +546,7 @@ selective_scan_bwd_sum_kernel(SelScanBwdArgs b, int gtiles, int ctas, long nB, l
         if (c) i -= nB;
         const float *p = (c ? b.part_C : b.part_B) + i;
         float s = 0.f;
+#pragma unroll 8
         for (int q = 0; q < gtiles; ++q) s += p[q * nB];
         st_act(c ? b.dC : b.dB, i, s, a.in_bf16);
         return;
@@ -571,6 +572,7 @@ selective_scan_bwd_sum_kernel(SelScanBwdArgs b, int gtiles, int ctas, long nB, l
     }
     if (!out) return;
     float s = 0.f;
+#pragma unroll 8
     for (int q = 0; q < ctas; ++q) s += p[q * n + i];
     out[i] = s;
 }

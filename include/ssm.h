@@ -569,7 +569,7 @@ SSM_API size_t selective_scan_workspace_size(int nseq, long long ntokens, int di
  * and in a fixed order: equal calls give equal bits.  Where the clamp of the
  * step size is active its gradient is zero.
  *   workspace     selective_scan_bwd_workspace_size(...) bytes, required.
- * Two launches.
+ * Two launches, three where sequences are cut into segments to fill the device.
  */
 SSM_API int selective_scan_bwd(int nseq, int seqlen, const int32_t *cu_seqlens, int dim,
                                int d_state, int ngroups, int in_dtype,

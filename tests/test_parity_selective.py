@@ -752,3 +752,66 @@ def test_offsets_beyond_32_bits():
     table = i32(slots - 3)
     assert ssm.ssm_pool_compact(pool, table).item() == 1 and table.item() == 0
     close(pool[0], wT[0], mT[0], ref.scan_rounding(p), "moved row")
+
+
+def test_two_streams_at_once():
+    """Calls that overlap on the GPU have outputs and workspaces of their own."""
+    from hybrid_mamba_ssm_b200 import ssm
+    cases = [scan_case(81 + k, [700, 300], 24, 16) for k in range(2)]
+    ops = [operands(p, "bf16", "bf16") for p in cases]
+    cu = cu_of(cases[0])
+
+    def step(k):
+        args, kw = ops[k]
+        y, h, saved = ssm.selective_scan_fwd(*args, **kw, cu_seqlens=cu, save_states=True)
+        return [y, h, *[t for t in ssm.selective_scan_bwd(args[0], *args, saved, **kw, cu_seqlens=cu) if t is not None]]
+
+    want = [step(0), step(1)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = []
+    for _ in range(6):
+        for k, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got.append((k, step(k)))
+    torch.cuda.synchronize()
+    for k, out in got:
+        for t, u in zip(out, want[k]):
+            assert torch.equal(t, u)
+
+
+def test_binding_names_what_is_wrong():
+    from hybrid_mamba_ssm_b200 import ssm
+    p = scan_case(91, [30], 32, 16)
+    (x, d, A, B, C), kw = operands(p, "bf16", "bf16")
+    cu = cu_of(p)
+    f = lambda *a, **k: ssm.selective_scan_fwd(*a, **{**kw, "cu_seqlens": cu, **k})  # noqa: E731
+    for bad in [(x.t(), d, A, B, C), (x, d[:10], A, B, C), (x, d, A[:, :3], B, C), (x, d, A, B[:, :, :4], C),
+                (x[:, ::2], d, A, B, C), (x, d.cpu(), A, B, C)]:
+        with pytest.raises(ValueError):
+            f(*bad)
+    for bad, k in [((x.half(), d, A, B, C), {}), ((x, d, A.double(), B, C), {}), ((x, d, A, B.float(), C), {}),
+                   ((x, d, A, B, C), dict(initial_state=torch.zeros(1, 32, 16, dtype=BF, device="cuda")))]:
+        with pytest.raises(TypeError):
+            f(*bad, **k)
+    for k in [dict(cu_seqlens=cu.cpu()), dict(slot_idx=cu[:1]), dict(workspace="no"), dict(D=kw["D"][:5]),
+              dict(y=torch.empty(30, 31, dtype=BF, device="cuda")), dict(final_state=torch.zeros(2, 32, 16, device="cuda"))]:
+        with pytest.raises(ValueError):
+            f(x, d, A, B, C, **k)
+    with pytest.raises(ssm.SSMError):                       # every token at one address
+        f(x[:1].expand(30, 32), d, A, B, C)
+    with pytest.raises(ssm.SSMError):                       # an output over an input
+        f(x, d, A, B, C, y=x)
+    with pytest.raises(ssm.SSMError):                       # fp32 activations with bf16 dt
+        f(x.float(), d, A, B.float(), C.float(), z=kw["z"].float())
+    saved = f(x, d, A, B, C, save_states=True)[2]
+    with pytest.raises(ValueError):
+        ssm.selective_scan_bwd(x, x, d, A, B, C, saved[:-1].clone(), **kw, cu_seqlens=cu)
+    with pytest.raises(ValueError):
+        ssm.selective_state_update(torch.zeros(30, 32, 8, device="cuda"), x, d, A, B, C)
+    with pytest.raises(ValueError):
+        ssm.causal_conv1d_bwd(x[:5], x, torch.zeros(32, 4, device="cuda"), cu_seqlens=cu)
+    with pytest.raises(ValueError):
+        ssm.causal_conv1d_bwd(x, x, torch.zeros(32, 4, device="cuda"), cu_seqlens=cu, activation="relu")
+    y, _ = f(x, d, A, B, C)                                 # and the context is as it was
+    assert bool(y.isfinite().all())
