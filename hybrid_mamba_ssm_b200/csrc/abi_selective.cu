@@ -5,6 +5,8 @@
 // between calls.
 #include "abi_checks.h"
 
+#include "../../include/ssm_testing.h"
+
 namespace {
 
 // One activation operand: rows of `width` elements, `stride` elements apart.
@@ -263,6 +265,13 @@ int selective_state_update(int batch, int dim, int d_state, int ngroups, float *
     a.x_stride = x_stride; a.dt_stride = dt_stride; a.B_stride = B_stride; a.C_stride = C_stride; a.z_stride = z_stride;
     a.A = A; a.D = D; a.dtp = dtp; a.y = y; a.status_dev = status_dev;
     return ssm::launch_selective_update(a, stream) == cudaSuccess ? SSM_OK : SSM_ERR_CUDA;
+}
+
+int ssm_testing_selective_bwd_rows(int nseq, int seqlen, int packed, int dim, int d_state, int ngroups, int *held)
+{
+    if (!held || nseq <= 0 || seqlen < 0 || dim <= 0 || d_state <= 0 || d_state > 256 || ngroups <= 0 || dim % ngroups)
+        return -1;
+    return ssm::selective_scan_bwd_rows(nseq, seqlen, packed != 0, dim, d_state, ngroups, held);
 }
 
 size_t causal_conv1d_bwd_workspace_size(long long ntokens, int dim, int width)

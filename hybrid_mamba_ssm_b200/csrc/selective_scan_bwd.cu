@@ -686,7 +686,25 @@ cudaError_t launch_types(const SelScanBwdArgs &b, const BwdPlan &p, cudaStream_t
     return launch_sets<TIn, TDt, 8, 32>(b, p, stream);
 }
 
+// The plan that a call runs: the one that sized the workspace, but without its cuts where equal lengths leave
+// nothing to cut.
+BwdPlan launch_plan(int nseq, int seqlen, bool packed, int dim, int d_state, int ngroups)
+{
+    BwdPlan p = make_plan(nseq, packed ? (long)seqlen : (long)nseq * seqlen, dim, d_state, ngroups);
+    if (p.span && !packed && p.span >= seqlen) {
+        p.span = 0;
+        p.ctas = p.units = nseq;
+    }
+    return p;
+}
+
 }  // namespace
+
+int selective_scan_bwd_rows(int nseq, int seqlen, bool packed, int dim, int d_state, int ngroups, int *held)
+{
+    *held = make_plan(nseq, packed ? (long)seqlen : (long)nseq * seqlen, dim, d_state, ngroups).ctas;
+    return launch_plan(nseq, seqlen, packed, dim, d_state, ngroups).ctas;
+}
 
 size_t selective_scan_bwd_workspace(int nseq, long T, int dim, int d_state, int ngroups)
 {
@@ -698,11 +716,7 @@ cudaError_t launch_selective_scan_bwd(SelScanBwdArgs b, void *workspace, cudaStr
     SelScanArgs &a = b.f;
     const long T = a.cu_seqlens ? (long)a.seqlen : (long)a.nseq * a.seqlen;
     const int N = a.d_state;
-    BwdPlan p = make_plan(a.nseq, T, a.dim, N, a.ngroups);
-    if (!a.cu_seqlens && p.span >= a.seqlen) {       // equal lengths, nothing to cut (the workspace stays as it is)
-        p.span = 0;
-        p.ctas = p.units = a.nseq;
-    }
+    const BwdPlan p = launch_plan(a.nseq, a.seqlen, a.cu_seqlens != nullptr, a.dim, N, a.ngroups);
     char *w = static_cast<char *>(workspace);
     auto take = [&](size_t bytes) {
         float *f = reinterpret_cast<float *>(w);

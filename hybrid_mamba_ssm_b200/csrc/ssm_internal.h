@@ -190,6 +190,7 @@ struct SelScanBwdArgs {
 int segment_span(int nseq, long T, double fill, bool ragged);
 int selective_scan_segments(int nseq, long T, int dim, int d_state, int ngroups, int *span);
 cudaError_t launch_selective_scan(const SelScanArgs &a, cudaStream_t stream);
+int selective_scan_bwd_rows(int nseq, int seqlen, bool packed, int dim, int d_state, int ngroups, int *held);
 size_t selective_scan_bwd_workspace(int nseq, long T, int dim, int d_state, int ngroups);
 cudaError_t launch_selective_scan_bwd(SelScanBwdArgs a, void *workspace, cudaStream_t stream);
 

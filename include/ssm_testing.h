@@ -23,7 +23,9 @@
  *
  * ssm_testing_balanced_runs exposes, for host-only tests, the rule by which
  * ssd_chunk_scan_workspace_size decides whether a fixed-length batch gets
- * the balanced schedule, for a device of a given SM count.
+ * the balanced schedule, for a device of a given SM count, and
+ * ssm_testing_selective_bwd_rows how many rows of the workspace a gradient
+ * of the per-channel scan uses.
  */
 #ifndef LIBSSM_SSM_TESTING_H
 #define LIBSSM_SSM_TESTING_H
@@ -74,6 +76,16 @@ SSM_API int ssm_testing_conv1d_stalled(int nseq, int seqlen, int dim, int width,
                                        const void *x, const float *weight, void *y,
                                        unsigned long long wait_ns, int *status_dev,
                                        cudaStream_t stream);
+
+/*
+ * ssm_testing_selective_bwd_rows -- the rows of partial sums of dA, dD and
+ * ddt_bias that a selective_scan_bwd of these sizes writes (packed: seqlen
+ * tokens in all), with in *held the rows that
+ * selective_scan_bwd_workspace_size counts for them; -1 for malformed sizes.
+ * Host arithmetic only; without a device that of a B200.
+ */
+SSM_API int ssm_testing_selective_bwd_rows(int nseq, int seqlen, int packed, int dim, int d_state,
+                                           int ngroups, int *held);
 
 #ifdef __cplusplus
 }
