@@ -114,6 +114,13 @@ __device__ __forceinline__ float min_nan(float a, float b) {   // NaN if either 
     asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
     return r;
 }
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+// A NaN stays one: fminf and fmaxf would make it the lower bound.
+__device__ __forceinline__ float clamp_nan(float v, float lo, float hi) { return min_nan(max_nan(v, lo), hi); }
 
 // e^-a for a >= 0 to about an ulp: 2^t with the rounding of t = -a log2 e
 // carried as a first-order correction.
@@ -144,7 +151,7 @@ __device__ __forceinline__ float log1p_unit(float e) {
 __device__ __forceinline__ float dt_value(const DtParams &p, float raw, float bias) {
     float v = raw + bias;
     if (p.softplus) v = fmaxf(v, 0.f) + log1p_unit(exp_neg(min_nan(fabsf(v), 120.f)));
-    if (p.clamp) v = fminf(fmaxf(v, p.lo), p.hi);
+    if (p.clamp) v = clamp_nan(v, p.lo, p.hi);
     return v;
 }
 __device__ __forceinline__ float dt_slope(const DtParams &p, float raw, float bias) {
@@ -174,8 +181,7 @@ __device__ __forceinline__ f32x2 dt_value2(const DtParams &p, f32x2 raw, f32x2 b
         for (int i = 8; i >= 0; --i) q = fma2(q, e, pack2(kLog1p[i], kLog1p[i]));
         v = fma2(q, e, pack2(fmaxf(lo2(v), 0.f), fmaxf(hi2(v), 0.f)));
     }
-    if (p.clamp)
-        v = pack2(fminf(fmaxf(lo2(v), p.lo), p.hi), fminf(fmaxf(hi2(v), p.lo), p.hi));
+    if (p.clamp) v = pack2(clamp_nan(lo2(v), p.lo, p.hi), clamp_nan(hi2(v), p.lo, p.hi));
     return v;
 }
 __device__ __forceinline__ f32x2 dt_slope2(const DtParams &p, f32x2 raw, f32x2 bias) {
