@@ -34,6 +34,19 @@ __device__ __forceinline__ void store_out(__nv_bfloat16 *p, float v) {
     *p = __float2bfloat16_rn(v);
 }
 
+__device__ __forceinline__ float min_nan(float a, float b) {   // NaN if either is
+    float r;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+// A NaN stays one: fminf and fmaxf would make it the lower bound.
+__device__ __forceinline__ float clamp_nan(float v, float lo, float hi) { return min_nan(max_nan(v, lo), hi); }
+
 // Step-size transform applied where a kernel reads dt (the raw projection
 // output): v = dt + bias[h]; v = log(1 + e^v) if softplus (v itself above
 // 20, where the two agree to fp32); clamp to [lo, hi] if clamp.  All off is
@@ -47,7 +60,7 @@ struct DtParams {
 __device__ __forceinline__ float dt_apply(const DtParams &p, float v, int h) {
     if (p.bias) v += __ldg(p.bias + h);
     if (p.softplus) v = v > 20.f ? v : log1pf(__expf(v));
-    if (p.clamp) v = fminf(fmaxf(v, p.lo), p.hi);
+    if (p.clamp) v = clamp_nan(v, p.lo, p.hi);
     return v;
 }
 

@@ -109,19 +109,6 @@ __device__ __forceinline__ int reduce_lanes(float (&v)[TG], int lane) {
     return first;
 }
 
-__device__ __forceinline__ float min_nan(float a, float b) {   // NaN if either is
-    float r;
-    asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-    return r;
-}
-__device__ __forceinline__ float max_nan(float a, float b) {
-    float r;
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-    return r;
-}
-// A NaN stays one: fminf and fmaxf would make it the lower bound.
-__device__ __forceinline__ float clamp_nan(float v, float lo, float hi) { return min_nan(max_nan(v, lo), hi); }
-
 // e^-a for a >= 0 to about an ulp: 2^t with the rounding of t = -a log2 e
 // carried as a first-order correction.
 __device__ __forceinline__ float exp_neg(float a) {
