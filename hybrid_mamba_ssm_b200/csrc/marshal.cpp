@@ -50,7 +50,12 @@ struct Args {
         want(t != nullptr);
         return *t;
     }
-    bool flag() { return PyObject_IsTrue(next()) == 1; }
+    // what has no truth value is the slow path's to name, before anything is launched
+    bool flag() {
+        const int v = PyObject_IsTrue(next());
+        want(v >= 0);
+        return v == 1;
+    }
 };
 
 int code_of(at::ScalarType t) {
