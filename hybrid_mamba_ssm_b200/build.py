@@ -14,6 +14,7 @@ import shutil
 import subprocess
 import sys
 import sysconfig
+import warnings
 from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -70,21 +71,31 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
             print(" ".join(cmd), flush=True)
         subprocess.check_call(cmd)
         os.replace(tmp, LIB)
-    build_marshal(force, verbose)
+    try:
+        build_marshal(force, verbose)
+    except (ImportError, OSError, subprocess.CalledProcessError) as e:
+        # ssm.py does without it; one of an earlier build may not fit this library
+        if os.path.exists(MARSHAL):
+            os.remove(MARSHAL)
+        warnings.warn(f"_marshal.so could not be built ({e}): calls take more host time", RuntimeWarning, stacklevel=2)
     return LIB
 
 
 def build_marshal(force: bool = False, verbose: bool = False) -> str:
-    """Compile csrc/marshal.cpp into _marshal.so (host code only)."""
-    src = os.path.join(CSRC, "marshal.cpp")
-    if not force and not _stale(MARSHAL, [src, os.path.join(ROOT, "include", "ssm.h")]):
-        return MARSHAL
+    """Compile csrc/marshal.cpp into _marshal.so (host code only, for this torch)."""
     import torch
+    src = os.path.join(CSRC, "marshal.cpp")
+    stamp = os.path.join(BUILD_DIR, "marshal.torch")     # the torch that _marshal.so was built for
+    built_for = open(stamp).read() if os.path.exists(stamp) else None
+    if not force and built_for == str(torch.__version__) \
+            and not _stale(MARSHAL, [src, os.path.join(ROOT, "include", "ssm.h")]):
+        return MARSHAL
+    os.makedirs(BUILD_DIR, exist_ok=True)
     troot = os.path.dirname(torch.__file__)
     cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(_nvcc()))), "include")
     tmp = MARSHAL + f".tmp{os.getpid()}"
     cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
-           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           f'-DSSM_TORCH_VERSION="{torch.__version__}"', f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
            "-I" + os.path.join(ROOT, "include"), "-isystem", sysconfig.get_paths()["include"],
            "-isystem", os.path.join(troot, "include"),
            "-isystem", os.path.join(troot, "include", "torch", "csrc", "api", "include"), "-isystem", cuda,
@@ -94,6 +105,8 @@ def build_marshal(force: bool = False, verbose: bool = False) -> str:
         print(" ".join(cmd), flush=True)
     subprocess.check_call(cmd)
     os.replace(tmp, MARSHAL)
+    with open(stamp, "w") as f:
+        f.write(torch.__version__)
     return MARSHAL
 
 

@@ -448,4 +448,13 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_marshal", nullptr, -1, methods, n
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__marshal(void) { return PyModule_Create(&module); }
+#ifndef SSM_TORCH_VERSION
+#error "SSM_TORCH_VERSION: the torch.__version__ whose headers these are"
+#endif
+
+// torch_version: what it was built for; ssm.py uses it with no other.
+PyMODINIT_FUNC PyInit__marshal(void) {
+    PyObject *m = PyModule_Create(&module);
+    if (m && PyModule_AddStringConstant(m, "torch_version", SSM_TORCH_VERSION) < 0) Py_CLEAR(m);
+    return m;
+}

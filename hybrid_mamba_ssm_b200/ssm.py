@@ -10,6 +10,7 @@ from __future__ import annotations
 import contextlib
 import ctypes
 import os
+import warnings
 from typing import NamedTuple
 
 import torch
@@ -113,11 +114,36 @@ def _load():
 
 
 lib = _load()
-try:
-    from . import _marshal
-except ImportError as e:
-    raise ImportError("_marshal.so is not built or does not load; run "
-                      "`python -m hybrid_mamba_ssm_b200.build`") from e
+
+
+class _NoMarshal:
+    """In the place of the _marshal module where there is none for this torch: every call takes the Python path."""
+
+    @staticmethod
+    def _none(*args):
+        return None
+
+    scan_fwd = scan_bwd = state_update = conv1d_bwd = pool_copy = pool_zero = pool_compact = _none
+
+
+def _load_marshal():
+    """The C++ side of the per-channel and pool calls (host code only, built
+    against one torch).  Without it they launch the same kernels, with a few
+    times the host time a call."""
+    try:
+        from . import _marshal
+        built_for = getattr(_marshal, "torch_version", None)
+        if built_for == str(torch.__version__):
+            return _marshal
+        why = f"it was built for torch {built_for}, this is {torch.__version__}"
+    except ImportError as e:
+        why = str(e)
+    warnings.warn(f"_marshal.so is not used ({why}); calls take more host time.  To build it: "
+                  "`python -m hybrid_mamba_ssm_b200.build`", RuntimeWarning, stacklevel=2)
+    return _NoMarshal
+
+
+_marshal = _load_marshal()
 
 
 class DtParams(ctypes.Structure):
@@ -614,8 +640,8 @@ def ssm_gated_rmsnorm(y, z, weight, group_size: int, eps: float = 1e-5, out=None
 # Each call first goes to its function of the _marshal module, which does the
 # same checks and allocations in C++ for a call that is plainly right (tensors
 # of the current device, default stream and workspace).  It answers None for
-# anything else; the Python below then names what is wrong, or takes the
-# options that _marshal does not.
+# anything else (and where it is missing, _NoMarshal); the Python below then
+# names what is wrong, or takes the options that _marshal does not.
 # ---------------------------------------------------------------------------
 def _plain(answer, where):
     """Whether _marshal made the call (its results are `answer`); raises on a library error."""
