@@ -322,6 +322,9 @@ int causal_conv1d_bwd(int nseq, int seqlen, const int32_t *cu_seqlens, int dim, 
 
 namespace {
 
+// Slots of a pool and entries of an index list: the kernels step through both with 32-bit counters.
+constexpr int kMaxRows = 1 << 30;
+
 // Pools of a row operation, checked: no row overlaps the next, none overlaps
 // the index lists (lists[0 .. nlists)), no pool is listed twice.
 int read_pools(int npools, const ssm_pool *pools, int max_slots, const Range *lists, int nlists,
@@ -349,7 +352,7 @@ int ssm_pool_copy(int npools, const ssm_pool *pools, int max_slots, int npairs, 
                   const int32_t *dst_idx, int *status_dev, cudaStream_t stream)
 {
     if (npools < 0 || npairs < 0 || max_slots <= 0) return SSM_ERR_INVALID_ARG;
-    if (npools > SSM_MAX_POOLS) return SSM_ERR_UNSUPPORTED;
+    if (npools > SSM_MAX_POOLS || max_slots > kMaxRows || npairs > kMaxRows) return SSM_ERR_UNSUPPORTED;
     if (npools == 0 || npairs == 0) return SSM_OK;
     if (!pools || !src_idx || !dst_idx) return SSM_ERR_INVALID_ARG;
     if (!aligned16(src_idx) || !aligned16(dst_idx) || !aligned16(status_dev)) return SSM_ERR_MISALIGNED;
@@ -364,7 +367,7 @@ int ssm_pool_zero(int npools, const ssm_pool *pools, int max_slots, int nrows, c
                   int *status_dev, cudaStream_t stream)
 {
     if (npools < 0 || nrows < 0 || max_slots <= 0) return SSM_ERR_INVALID_ARG;
-    if (npools > SSM_MAX_POOLS) return SSM_ERR_UNSUPPORTED;
+    if (npools > SSM_MAX_POOLS || max_slots > kMaxRows || nrows > kMaxRows) return SSM_ERR_UNSUPPORTED;
     if (npools == 0 || nrows == 0) return SSM_OK;
     if (!pools || !row_idx) return SSM_ERR_INVALID_ARG;
     if (!aligned16(row_idx) || !aligned16(status_dev)) return SSM_ERR_MISALIGNED;
@@ -385,7 +388,7 @@ int ssm_pool_compact(int npools, const ssm_pool *pools, int max_slots, int nrows
                      cudaStream_t stream)
 {
     if (npools < 0 || nrows < 0 || max_slots <= 0) return SSM_ERR_INVALID_ARG;
-    if (npools > SSM_MAX_POOLS) return SSM_ERR_UNSUPPORTED;
+    if (npools > SSM_MAX_POOLS || max_slots > kMaxRows || nrows > kMaxRows) return SSM_ERR_UNSUPPORTED;
     if ((npools && !pools) || (nrows && !slot_idx) || !workspace) return SSM_ERR_INVALID_ARG;
     if (!aligned16(slot_idx) || !aligned16(nlive) || !aligned16(workspace) || !aligned16(status_dev))
         return SSM_ERR_MISALIGNED;

@@ -635,7 +635,8 @@ SSM_API size_t causal_conv1d_bwd_workspace_size(long long ntokens, int dim, int 
  * i in [0, max_slots): an SSM or conv pool of any type or layout whose slots
  * are contiguous.  Rows must not overlap, in a pool or between pools.  Index
  * lists are device int32, 16-byte aligned.  A negative index skips its entry;
- * one >= max_slots skips it and sets SSM_ERR_DEVICE_INPUT.
+ * one >= max_slots skips it and sets SSM_ERR_DEVICE_INPUT.  max_slots and the
+ * lengths of the lists are at most 2^30 (SSM_ERR_UNSUPPORTED beyond).
  */
 typedef struct {
     void *base;

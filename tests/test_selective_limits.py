@@ -28,3 +28,17 @@ def test_gradient_stays_inside_the_rows_its_workspace_holds(lib, packed):
         tokens = nseq * seqlen if packed else seqlen
         rows = lib.ssm_testing_selective_bwd_rows(nseq, tokens, packed, dim, N, G, ctypes.byref(held))
         assert 0 < rows <= held.value, (nseq, seqlen, dim, N, G, rows, held.value)
+
+
+def test_pool_calls_refuse_what_their_counters_do_not_hold(lib):
+    """Slots and index lists of more than 2^30 entries: the steps of the kernels' loops would pass 2^31."""
+    M, most, UNSUPPORTED = 1 << 24, 1 << 30, 2
+    one = (ctypes.c_int64 * 3)(M, 1, 1)
+    table, work = 1 << 44, 1 << 45                          # fake addresses: refused before anything is read
+    for slots, n in ((most + 1, 4), (2 ** 31 - 1, 4), (4, most + 1), (4, 2 ** 31 - 1)):
+        assert lib.ssm_pool_copy(1, one, slots, n, table, table, None, None) == UNSUPPORTED
+        assert lib.ssm_pool_zero(1, one, slots, n, table, None, None) == UNSUPPORTED
+        assert lib.ssm_pool_compact(1, one, slots, n, table, None, work, 1 << 40, None, None) == UNSUPPORTED
+    # at the limit it is the next check that answers
+    assert lib.ssm_pool_copy(1, one, most, most, table + 4, table, None, None) == 3
+    assert lib.ssm_pool_compact(1, one, most, most, table, None, work, 16, None, None) == 1
