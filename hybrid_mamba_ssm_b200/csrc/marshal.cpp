@@ -31,6 +31,12 @@ void want(bool ok) {
     if (!ok) throw NotPlain();
 }
 
+// A size as the ABI takes it; Python names one that does not fit.
+int count(int64_t v) {
+    want(v >= 0 && v <= 0x7fffffff);
+    return (int)v;
+}
+
 // The arguments of a call, in order.
 struct Args {
     PyObject *const *p;
@@ -141,7 +147,7 @@ struct Tokens {
             T = nseq * seqlen;
             dim = x.size(2);
         }
-        want(T <= 0x7fffffff && dim <= 0x7fffffff && nseq <= 0x7fffffff);
+        count(T);
     }
     at::IntArrayRef axes() const { return at::IntArrayRef(lead, nlead); }
 };
@@ -257,15 +263,15 @@ PyObject *scan_fwd(PyObject *, PyObject *const *p, Py_ssize_t n) {
         }
         size_t wsb = 0;
         if (save) {
-            saved = fresh(x, {(int64_t)(selective_scan_saved_size((int)t.nseq, t.T, (int)t.dim, (int)o.N) / 4)}, at::kFloat);
+            saved = fresh(x, {(int64_t)(selective_scan_saved_size(count(t.nseq), t.T, count(t.dim), count(o.N)) / 4)}, at::kFloat);
         }
-        if ((wsb = selective_scan_workspace_size((int)t.nseq, t.T, (int)t.dim, (int)o.N, (int)o.G))) {
+        if ((wsb = selective_scan_workspace_size(count(t.nseq), t.T, count(t.dim), count(o.N), count(o.G)))) {
             ws = fresh(x, {(int64_t)wsb}, at::kByte);
         }
         const int st = selective_scan_fwd(
-            (int)t.nseq, (int)t.seqlen, t.cu, (int)t.dim, (int)o.N, (int)o.G, o.in_code, o.x.p, o.x.stride, o.dt_code, o.dt.p,
+            count(t.nseq), count(t.seqlen), t.cu, count(t.dim), count(o.N), count(o.G), o.in_code, o.x.p, o.x.stride, o.dt_code, o.dt.p,
             o.dt.stride, o.A, o.B.p, o.B.stride, o.C.p, o.C.stride, o.D, o.z.p, o.z.stride, o.dt_params(), dev.f32(init, state),
-            static_cast<float *>(dev.data(fin, at::kFloat, state)), (int)state[0], dev.i32(slots, seqs), dev.i32(has, seqs),
+            static_cast<float *>(dev.data(fin, at::kFloat, state)), count(state[0]), dev.i32(slots, seqs), dev.i32(has, seqs),
             code_of(y->scalar_type()), dev.data(*y, y->scalar_type(), x.sizes()), static_cast<float *>(addr(saved)), addr(ws), wsb,
             dev.status(status), dev.stream());
         return result(st, {ref(y), ref(fin), wrap(saved)});
@@ -287,7 +293,7 @@ PyObject *scan_bwd(PyObject *, PyObject *const *p, Py_ssize_t n) {
         const int64_t row[1] = {t.dim}, state[3] = {t.nseq, t.dim, o.N}, an[2] = {t.dim, o.N};
         const at::ScalarType type = x.scalar_type();
         const Rows dy(dev, tdy, type, t.axes(), row);
-        want((size_t)saved.numel() * 4 == selective_scan_saved_size((int)t.nseq, t.T, (int)t.dim, (int)o.N));
+        want((size_t)saved.numel() * 4 == selective_scan_saved_size(count(t.nseq), t.T, count(t.dim), count(o.N)));
         std::vector<int64_t> bc(t.lead, t.lead + t.nlead);
         bc.push_back(o.G);
         bc.push_back(o.N);
@@ -297,10 +303,10 @@ PyObject *scan_bwd(PyObject *, PyObject *const *p, Py_ssize_t n) {
         if (o.gate) dz = fresh(x, x.sizes(), type);
         if (o.params.dt_bias) db = fresh(x, row, at::kFloat);
         if (want_init) di = fresh(x, state, at::kFloat);
-        const size_t wsb = selective_scan_bwd_workspace_size((int)t.nseq, t.T, (int)t.dim, (int)o.N, (int)o.G);
+        const size_t wsb = selective_scan_bwd_workspace_size(count(t.nseq), t.T, count(t.dim), count(o.N), count(o.G));
         Tensor ws = fresh(x, {(int64_t)wsb}, at::kByte);
         const int st = selective_scan_bwd(
-            (int)t.nseq, (int)t.seqlen, t.cu, (int)t.dim, (int)o.N, (int)o.G, o.in_code, dy.p, dy.stride, o.x.p, o.x.stride,
+            count(t.nseq), count(t.seqlen), t.cu, count(t.dim), count(o.N), count(o.G), o.in_code, dy.p, dy.stride, o.x.p, o.x.stride,
             o.dt_code, o.dt.p, o.dt.stride, o.A, o.B.p, o.B.stride, o.C.p, o.C.stride, o.D, o.z.p, o.z.stride, o.dt_params(),
             dev.f32(&saved, saved.sizes()), dev.f32(dfin, state), dx.data_ptr(), ddt.data_ptr(), static_cast<float *>(dA.data_ptr()),
             dB.data_ptr(), dC.data_ptr(), static_cast<float *>(addr(dD)), addr(dz), static_cast<float *>(addr(db)),
@@ -314,7 +320,7 @@ PyObject *state_update(PyObject *, PyObject *const *p, Py_ssize_t n) {
     return guarded([](Args &a) {
         const Tensor &x = a.tensor();
         const Device dev(x);
-        want(x.dim() == 2 && x.size(0) <= 0x7fffffff && x.size(1) <= 0x7fffffff);
+        want(x.dim() == 2);
         const int64_t lead[1] = {x.size(0)}, dim = x.size(1);
         const Operands o(dev, a, x, lead, dim);
         const Tensor &state = a.tensor(), *slots = a.optional(), *y = a.optional(), *status = a.optional();
@@ -326,7 +332,7 @@ PyObject *state_update(PyObject *, PyObject *const *p, Py_ssize_t n) {
             y = &made;
         }
         const int st = selective_state_update(
-            (int)lead[0], (int)dim, (int)o.N, (int)o.G, static_cast<float *>(dev.data(state, at::kFloat, rows)), (int)rows[0],
+            count(lead[0]), count(dim), count(o.N), count(o.G), static_cast<float *>(dev.data(state, at::kFloat, rows)), count(rows[0]),
             dev.i32(slots, lead), o.in_code, o.x.p, o.x.stride, o.dt_code, o.dt.p, o.dt.stride, o.A, o.B.p, o.B.stride, o.C.p,
             o.C.stride, o.D, o.z.p, o.z.stride, o.dt_params(), code_of(y->scalar_type()), dev.data(*y, y->scalar_type(), x.sizes()),
             dev.status(status), dev.stream());
@@ -349,10 +355,10 @@ PyObject *conv1d_bwd(PyObject *, PyObject *const *p, Py_ssize_t n) {
         Tensor dx = fresh(x, x.sizes(), type), dw = fresh(x, wk, at::kFloat), db, di;
         if (bias) db = fresh(x, row, at::kFloat);
         if (init) di = fresh(x, line, type);
-        const size_t wsb = causal_conv1d_bwd_workspace_size(t.T, (int)t.dim, (int)K);
+        const size_t wsb = causal_conv1d_bwd_workspace_size(t.T, count(t.dim), count(K));
         Tensor ws = fresh(x, {(int64_t)wsb}, at::kByte);
         const int st = causal_conv1d_bwd(
-            (int)t.nseq, (int)t.seqlen, t.cu, (int)t.dim, (int)K, code_of(type), dev.data(dy, type, x.sizes()),
+            count(t.nseq), count(t.seqlen), t.cu, count(t.dim), count(K), code_of(type), dev.data(dy, type, x.sizes()),
             dev.data(x, type, x.sizes()), dev.f32(&w, wk), dev.f32(bias, row), (int)act, dev.data(init, type, line),
             dev.data(dfin, type, line), dx.data_ptr(), static_cast<float *>(dw.data_ptr()), static_cast<float *>(addr(db)), addr(di),
             wsb ? ws.data_ptr() : nullptr, wsb, dev.status(status), dev.stream());
@@ -385,7 +391,7 @@ struct Pools {
         if (!first) {
             first = &t;
             slots = t.size(0);
-            want(slots > 0 && slots <= 0x7fffffff);
+            want(slots > 0);
         }
         want(t.get_device() == first->get_device() && t.size(0) == slots);
         int64_t step = 1;
@@ -405,7 +411,7 @@ PyObject *pool_copy(PyObject *, PyObject *const *p, Py_ssize_t n) {
         const Device dev(*q.first);
         const Tensor &src = a.tensor(), &dst = a.tensor(), *status = a.optional();
         want(src.dim() == 1);
-        const int st = ssm_pool_copy((int)q.rows.size(), q.rows.data(), (int)q.slots, (int)src.size(0), dev.i32(&src, src.sizes()),
+        const int st = ssm_pool_copy(count(q.rows.size()), q.rows.data(), count(q.slots), count(src.size(0)), dev.i32(&src, src.sizes()),
                                      dev.i32(&dst, src.sizes()), dev.status(status), dev.stream());
         return result(st, {});
     }, p, n);
@@ -418,7 +424,7 @@ PyObject *pool_zero(PyObject *, PyObject *const *p, Py_ssize_t n) {
         const Device dev(*q.first);
         const Tensor &rows = a.tensor(), *status = a.optional();
         want(rows.dim() == 1);
-        const int st = ssm_pool_zero((int)q.rows.size(), q.rows.data(), (int)q.slots, (int)rows.size(0),
+        const int st = ssm_pool_zero(count(q.rows.size()), q.rows.data(), count(q.slots), count(rows.size(0)),
                                      dev.i32(&rows, rows.sizes()), dev.status(status), dev.stream());
         return result(st, {});
     }, p, n);
@@ -433,9 +439,9 @@ PyObject *pool_compact(PyObject *, PyObject *const *p, Py_ssize_t n) {
         want(table.dim() == 1);
         int32_t *slots = static_cast<int32_t *>(dev.data(table, at::kInt, table.sizes()));
         Tensor live = fresh(table, {}, at::kInt);
-        const size_t wsb = ssm_pool_compact_workspace_size((int)q.slots, (int)table.size(0));
+        const size_t wsb = ssm_pool_compact_workspace_size(count(q.slots), count(table.size(0)));
         Tensor ws = fresh(table, {(int64_t)wsb}, at::kByte);
-        const int st = ssm_pool_compact((int)q.rows.size(), q.rows.data(), (int)q.slots, (int)table.size(0), slots,
+        const int st = ssm_pool_compact(count(q.rows.size()), q.rows.data(), count(q.slots), count(table.size(0)), slots,
                                         static_cast<int32_t *>(live.data_ptr()), ws.data_ptr(), wsb, dev.status(status), dev.stream());
         return result(st, {wrap(live)});
     }, p, n);

@@ -692,6 +692,13 @@ def _dev_like(t, name, dev, dtype=None, shape=None):
     raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
+def _count(n, name):
+    """n as the ABI takes it (ctypes would drop the bits above an int's)."""
+    if n > 0x7fffffff:
+        raise ValueError(f"{name} is {n}: at most 2^31 - 1 are supported")
+    return n
+
+
 def _token_rows(t, name, lead, row, dev, dtype):
     """Elements between the tokens of an activation of shape lead + row (lead:
     (T,), or (nseq, L)), whose rows are contiguous and equally spaced."""
@@ -723,11 +730,13 @@ def _scan_lead(x, cu_seqlens, dev):
         _dev_like(cu_seqlens, "cu_seqlens", dev, _I32)
         if x.dim() != 2 or cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 1:
             raise ValueError("packed x must be [T, dim] with cu_seqlens [nseq+1]")
-        T, dim = x.shape
-        return (T,), cu_seqlens.shape[0] - 1, T, T, dim
+        T, dim = _count(x.shape[0], "the number of tokens"), _count(x.shape[1], "dim")
+        return (T,), _count(cu_seqlens.shape[0] - 1, "the number of sequences"), T, T, dim
     if x.dim() != 3:
         raise ValueError("x must be [nseq, L, dim], or [T, dim] with cu_seqlens")
     n, length, dim = x.shape
+    for v, name in ((n, "the number of sequences"), (length, "the sequence length"), (dim, "dim")):
+        _count(v, name)
     return (n, length), n, length, n * length, dim
 
 
@@ -738,7 +747,7 @@ def _scan_operands(lead, dim, dev, x, dt, A, B, C, D, z, dt_bias, dt_softplus, d
     in_code, dt_code = _dtype_code(dtype), _dtype_code(dt.dtype)
     if A.dim() != 2 or B.dim() != len(lead) + 2:
         raise ValueError("A must be [dim, d_state], B and C the tokens' [ngroups, d_state]")
-    N, G = A.shape[1], B.shape[-2]
+    N, G = _count(A.shape[1], "d_state"), _count(B.shape[-2], "ngroups")
     row, bc = (dim,), (G, N)
     a = _dev_like(A, "A", dev, _F32, (dim, N))
     d = _dev_like(D, "D", dev, _F32, row)
@@ -805,7 +814,7 @@ def selective_scan_fwd(x, dt, A, B, C, D=None, z=None, initial_state=None, cu_se
             states = final_state if final_state is not None else initial_state
             if states is None:
                 raise ValueError("slot_idx needs a state pool")
-            rows = states.shape[0]
+            rows = _count(states.shape[0], "max_slots")
         elif final_state is None and return_final_state:
             final_state = x.new_empty((nseq, dim, N), dtype=_F32)
         if y is None:
@@ -911,10 +920,10 @@ def selective_state_update(state, x, dt, A, B, C, D=None, z=None, slot_idx=None,
         if x.dim() != 2:
             raise ValueError("x must be [batch, dim]")
         dev = x.get_device()
-        batch, dim = x.shape
+        batch, dim = _count(x.shape[0], "batch"), _count(x.shape[1], "dim")
         N, G, in_code, operands = _scan_operands((batch,), dim, dev, x, dt, A, B, C, D, z, dt_bias, dt_softplus,
                                                  dt_limit)
-        rows = batch if slot_idx is None else state.shape[0]
+        rows = batch if slot_idx is None else _count(state.shape[0], "max_slots")
         if y is None:
             y = x.new_zeros((batch, dim), dtype=y_dtype or x.dtype)
         st = lib.selective_state_update(
@@ -944,7 +953,7 @@ def causal_conv1d_bwd(dy, x, weight, bias=None, initial_state=None, dfinal_state
         _, nseq, seqlen, T, dim = _scan_lead(x, cu_seqlens, dev)
         if weight.dim() != 2:
             raise ValueError("weight must be [dim, width]")
-        width = weight.shape[1]
+        width = _count(weight.shape[1], "width")
         dx, dweight = x.new_empty(x.shape), weight.new_empty((dim, width))
         dbias = None if bias is None else weight.new_empty((dim,))
         line = (nseq, dim, width - 1)
@@ -969,7 +978,7 @@ def _pools(pools):
     if not pools:
         raise ValueError("no pools given")
     first = pools[0]
-    dev, slots = first.get_device(), first.shape[0] if first.dim() else -1
+    dev, slots = first.get_device(), _count(first.shape[0], "max_slots") if first.dim() else -1
     fields, shape, strides, size = [], None, None, 0
     for p in pools:
         # the pools of a stack's layers are mostly alike: a layout is looked at once
@@ -999,7 +1008,7 @@ def ssm_pool_copy(pools, src_idx, dst_idx, status=None, stream=None) -> None:
         return
     arr, n, slots, like = _pools(pools)
     with _scope(like, stream):
-        dev, pairs = like.get_device(), src_idx.shape[0]
+        dev, pairs = like.get_device(), _count(src_idx.shape[0], "the number of pairs")
         st = lib.ssm_pool_copy(n, arr, slots, pairs, _dev_like(src_idx, "src_idx", dev, _I32, (pairs,)),
                                _dev_like(dst_idx, "dst_idx", dev, _I32, (pairs,)),
                                _dev_like(status, "status", dev, _I32), _raw_stream(dev))
@@ -1012,7 +1021,7 @@ def ssm_pool_zero(pools, row_idx, status=None, stream=None) -> None:
         return
     arr, n, slots, like = _pools(pools)
     with _scope(like, stream):
-        dev, rows = like.get_device(), row_idx.shape[0]
+        dev, rows = like.get_device(), _count(row_idx.shape[0], "the number of rows")
         st = lib.ssm_pool_zero(n, arr, slots, rows, _dev_like(row_idx, "row_idx", dev, _I32, (rows,)),
                                _dev_like(status, "status", dev, _I32), _raw_stream(dev))
     _check(st, "ssm_pool_zero")
@@ -1028,7 +1037,7 @@ def ssm_pool_compact(pools, slot_idx, status=None, stream=None, workspace="auto"
             return out[0]
     arr, n, slots, like = _pools(pools)
     with _scope(like, stream):
-        dev, rows = like.get_device(), slot_idx.shape[0]
+        dev, rows = like.get_device(), _count(slot_idx.shape[0], "the number of rows")
         live = slot_idx.new_empty(())
         size = lib.ssm_pool_compact_workspace_size(slots, rows) if isinstance(workspace, str) else 0
         ws, ws_ptr, ws_bytes = _workspace(workspace, size, like, dev)

@@ -4,6 +4,7 @@ import ctypes
 import itertools
 
 import pytest
+import torch
 
 from hybrid_mamba_ssm_b200 import build as ssm_build
 
@@ -42,3 +43,23 @@ def test_pool_calls_refuse_what_their_counters_do_not_hold(lib):
     # at the limit it is the next check that answers
     assert lib.ssm_pool_copy(1, one, most, most, table + 4, table, None, None) == 3
     assert lib.ssm_pool_compact(1, one, most, most, table, None, work, 16, None, None) == 1
+
+
+def test_binding_refuses_sizes_that_do_not_fit_an_int(lib):
+    """ctypes passes 2^32 + 8 as 8: such a size is named before it gets there (shapes only, nothing is allocated)."""
+    from hybrid_mamba_ssm_b200 import ssm
+    big = 2 ** 32 + 8
+    shape = lambda *s: torch.empty(s, device="meta")  # noqa: E731
+    cu = torch.zeros(2, dtype=torch.int32)
+    for x, offsets in ((shape(big, 4), cu), (shape(4, big), cu), (shape(big, 1, 4), None), (shape(1, big, 4), None),
+                       (shape(1, 4, big), None)):
+        with pytest.raises(ValueError, match="2\\^31"):
+            ssm._scan_lead(x, offsets, -1)
+    x = torch.zeros(4, 8)
+    for A, B in ((shape(8, big), shape(4, 1, big)), (shape(8, 2), shape(4, big, 2))):
+        with pytest.raises(ValueError, match="2\\^31"):
+            ssm._scan_operands((4,), 8, -1, x, x, A, B, B, None, None, None, False, None)
+    for pools in (shape(big, 1), [shape(big, 4), shape(big, 2)]):
+        with pytest.raises(ValueError, match="2\\^31"):
+            ssm._pools(pools)
+    assert ssm._pools(shape(2 ** 31 - 1, 1))[2] == 2 ** 31 - 1
