@@ -58,6 +58,14 @@ __device__ __forceinline__ f32x2 decay2(f32x2 v, f32x2 A) {
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
+// Decay rates in units of log2 e, kept finite: a token with a step size of 0
+// (the tokens that fill up a tile among them) has the decay 2^(0 A) = 1
+// whatever A is, and 0 * -inf would be NaN.
+__device__ __forceinline__ f32x2 decay_rate2(f32x2 A) {
+    const f32x2 r = mul2(A, pack2(kLog2e, kLog2e));
+    return pack2(max_nan(lo2(r), -3.402823466e38f), max_nan(hi2(r), -3.402823466e38f));
+}
+
 // NV consecutive fp32 values of shared memory (16-byte aligned for NV >= 4,
 // 8-byte for NV == 2) as packed pairs.
 template <int NP2>

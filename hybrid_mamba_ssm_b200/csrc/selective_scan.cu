@@ -152,7 +152,7 @@ selective_scan_kernel(SelScanArgs a)
         for (int p = 0; p < P; ++p) A[q][p] = pack2(0.f, 0.f);
         if (live(q)) load_states<R>(row_of(a.A, 0, q), j, N, A[q]);
 #pragma unroll
-        for (int p = 0; p < P; ++p) A[q][p] = mul2(A[q][p], pack2(kLog2e, kLog2e));
+        for (int p = 0; p < P; ++p) A[q][p] = decay_rate2(A[q][p]);
     }
     // Raw values of the next tile; x and z of the one whose output is due.
     RawPair<TIn, kPacked> xr[E], zr[E], xc[E], zc[E];

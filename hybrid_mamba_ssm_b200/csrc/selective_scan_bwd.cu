@@ -169,7 +169,7 @@ selective_scan_bwd_kernel(SelScanBwdArgs b, int ctas)
         for (int p = 0; p < P; ++p) A[q][p] = dA[q][p] = pack2(0.f, 0.f);
         if (d < cend) load_row<R>(a.A + (long)d * N, j, N, A[q]);
 #pragma unroll
-        for (int p = 0; p < P; ++p) A[q][p] = mul2(A[q][p], pack2(kLog2e, kLog2e));
+        for (int p = 0; p < P; ++p) A[q][p] = decay_rate2(A[q][p]);
     }
 
     __shared__ int s_seq;

@@ -1,9 +1,11 @@
 """Values that are not finite in the per-channel scan, its gradient and decode
 update: they reach what the definition lets them reach, and nothing else."""
+import numpy as np
 import pytest
 import torch
 
-from tests.test_parity_selective import cu_of, operands, scan_case
+from tests import selective_ref as ref
+from tests.test_parity_selective import close, cu_of, dev, operands, scan_case
 
 pytestmark = pytest.mark.gpu
 
@@ -37,3 +39,37 @@ def test_a_nan_step_size_passes_the_clamp(dim, softplus):
                                    dt_bias=kw["dt_bias"], dt_softplus=softplus, dt_limit=p["limit"])
     assert bool(u[1, c].isnan()) and bool(state[1, c].isnan().all())
     assert bool(u[1, rest].isfinite().all()) and bool(u[[0, 2]].isfinite().all())
+
+
+@pytest.mark.parametrize("rate", [float("-inf"), -3e38])
+@pytest.mark.parametrize("lens,dim,N", [([37, 5], 64, 16), ([33], 33, 13), ([1, 2, 3], 24, 64), ([1501], 16, 16)])
+def test_a_state_that_is_forgotten_at_once(lens, dim, N, rate):
+    """exp(v A) = 0 for a step size above 0 and a decay rate without bound (or one that overflows in other units):
+    the state is the last token's alone, whatever length fills the last tile."""
+    from hybrid_mamba_ssm_b200 import ssm
+    p = scan_case(131, lens, dim, N)
+    pick = np.random.default_rng(132).random(p["A"].shape) < 0.25
+    p["A"][pick] = rate
+    args, kw = operands(p, "bf16", "bf16")
+    cu = cu_of(p)
+    y, hT, saved = ssm.selective_scan_fwd(*args, **kw, initial_state=dev(p["h0"]), cu_seqlens=cu, save_states=True)
+    want, wT, *_ = ref.scan(p)
+    mag, mT, *_ = ref.scan(p, magnitude=True)
+    assert np.isfinite(want).all() and np.isfinite(wT).all()
+    close(y, want, mag, ref.scan_rounding(p), "y")
+    close(hT, wT, mT, ref.scan_rounding(p), "final state")
+    g = ssm.selective_scan_bwd(torch.ones_like(args[0]), *args, saved, **kw, cu_seqlens=cu, want_dinitial=True)
+    q = {**p, "A": np.where(pick, -1e30, p["A"])}           # the limit: no product 0 * inf in the reference
+    dy = np.ones_like(p["x"])
+    zero = np.zeros_like(p["h0"])
+    want, mag = ref.scan_grad(q, dy, zero), ref.scan_grad(q, dy, zero, magnitude=True)
+    n = ref.scan_rounding(p)
+    for t, k in [(g.dx, "dx"), (g.ddt, "ddt"), (g.dA, "dA"), (g.dB, "dB"), (g.dC, "dC"), (g.dinitial_state, "dh0")]:
+        close(t, want[k], mag[k], n + (sum(lens) + dim if k in ("dA", "dB", "dC") else 0), k)
+    state = dev(p["h0"])                                    # and one token
+    first = [p["cu"][i] for i in range(len(lens))]
+    x, d, A, B, C = args
+    ssm.selective_state_update(state, x[first], d[first], A, B[first], C[first], D=kw["D"], z=kw["z"][first],
+                               dt_bias=kw["dt_bias"], dt_softplus=True)
+    hs = ref.scan(p)[4][first]
+    close(state, hs, ref.scan(p, magnitude=True)[4][first], ref.scan_rounding(p), "state")
