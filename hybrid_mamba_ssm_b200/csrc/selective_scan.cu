@@ -19,10 +19,10 @@
 // left to the step that writes y.
 //
 // What bounds it (ncu, 4096 tokens of 8192 channels, 16 states, bf16): the
-// shared-memory pipe at 76 % of its cycles, of which B and C, read by every
-// lane for its own states, are two thirds; the special-function unit at 50 %
+// shared-memory pipe at 77 % of its cycles, of which B and C, read by every
+// lane for its own states, are two thirds; the special-function unit at 53 %
 // (one exponential an element and three a (token, channel): 0.28 ms for 4 x
-// 2048 tokens if it were the bound); issue slots at 57 %; HBM at 10 %.  4 x 2048
+// 2048 tokens if it were the bound); issue slots at 58 %; HBM at 11 %.  4 x 2048
 // tokens take 0.53 ms, 1 x 32768 of 2048 channels 0.90 ms.
 // Q = 2 halves the reads of B and C but also the warps: 0.62 ms against 0.53 at
 // 16 states, where seven CTAs an SM hide the latencies, but 0.48 against 0.63 ms

@@ -864,7 +864,9 @@ def selective_scan_bwd(dy, x, dt, A, B, C, saved, D=None, z=None, dfinal_state=N
     """Gradient of selective_scan_fwd called with the same inputs and
     save_states=True (`saved` is its third result).  dy : like x.
     dfinal_state : [nseq, dim, d_state] fp32 or None.  The gradients have their
-    inputs' shapes and types (contiguous)."""
+    inputs' shapes and types (contiguous).  The workspace grows with the square
+    of d_state (2 GiB for 8192 tokens of 8192 channels at 64 states, 8 at 128):
+    selective_scan_bwd_workspace_size says how large it is."""
     if stream is None and isinstance(workspace, str) and workspace == "auto":
         out = _marshal.scan_bwd(x, cu_seqlens, dt, A, B, C, D, z, dt_bias, dt_softplus, dt_limit, dy, saved,
                                 dfinal_state, want_dinitial, status)

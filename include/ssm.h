@@ -568,7 +568,17 @@ SSM_API size_t selective_scan_workspace_size(int nseq, long long ntokens, int di
  * [nseq][dim][d_state] (or NULL) in fp32.  dz goes with z.  Every sum is fp32
  * and in a fixed order: equal calls give equal bits.  Where the clamp of the
  * step size is active its gradient is zero.
- *   workspace     selective_scan_bwd_workspace_size(...) bytes, required.
+ * dinitial_state is the gradient of the state in front of a sequence's first
+ * token; a forward call with has_initial_state 0 for a sequence did not read
+ * that state from initial_state.  With nseq = 0 nothing is written.
+ *   workspace     selective_scan_bwd_workspace_size(...) bytes, required.  Most
+ *                 of it are parts of dB and dC, one of T * ngroups * d_state
+ *                 fp32 values each per tile of CB channels of a group, where CB
+ *                 is 128 at up to 4 states, 64 or 128 at 8, 32 or 64 at 16, 16
+ *                 or 32 at 32, 8 or 16 at 64, 4 or 8 at 128, and 4 above.  So
+ *                 it grows with the square of d_state: for 8192 tokens of 8192
+ *                 channels 0.14 GiB at 16 states, 2.0 at 64, 8.0 at 128, 32 at
+ *                 256.
  * Two launches, three where sequences are cut into segments to fill the device.
  */
 SSM_API int selective_scan_bwd(int nseq, int seqlen, const int32_t *cu_seqlens, int dim,
